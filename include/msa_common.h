@@ -9,6 +9,7 @@
  *   libmsa_decode.so  sparse decode attention          (msa_decode.h)
  *   libmsa_prefill.so the query's own tokens through sparse attention (msa_prefill.h)
  *   libmsa_bank.so    bank file save / load, append re-layout (msa_bank.h)
+ *   libmsa_paged.so   batches over one shared memory and a paged local cache (msa_paged.h)
  *
  * Conventions shared by every entry point:
  *  - Every call returns an msa_status; nothing else crosses the ABI on failure.  The
@@ -60,6 +61,7 @@ typedef struct CUstream_st* msa_stream_t;
                                       failed with no further stage to send it to (kept in
                                       the ABI; the routing's last stage is an exact scan,
                                       so msa_route_topk does not raise it) */
+#define MSA_DEVERR_BAD_PAGE 64u /* a page id outside [0, n_pages) (its rows skipped)      */
 
 /* Bytes of one memory block of one layer in a bf16 bank:
  * routing key H*d*2; content key + value 2*H*d*2. */

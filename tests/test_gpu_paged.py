@@ -1,0 +1,303 @@
+"""Paged batches on the GPU (include/msa_paged.h) against their definition in 64 bits.
+
+Tolerances are derived in paged_ref.py.  Slots and rows that no key occupies hold NaN in
+every case, and unused page-table entries an id outside the pool."""
+import pytest
+import torch
+
+import top_kv_routing_b200 as msa
+from paged_ref import D, Batch, rope
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------- append
+
+def _check_append(x, q_rot, before, pos_offset, pos, theta=1e6):
+    """Stored rows and rotated queries: half a bf16 step of the exact rotation, plus the fp32
+    rotation's own error (angles within 2^-22 of a half turn as sine and cosine, two products
+    and a sum: at most 2^-20 of |lo| + |hi|)."""
+    want = before.clone().double()
+    for b, (new, past) in enumerate(zip(x.new, x.past)):
+        if new == 0:
+            continue
+        t0 = x.off[b].item()
+        row = torch.arange(past, past + new, device=x.q.device)
+        at = (pos + int(pos_offset[b]) if pos_offset is not None else pos) + row
+        rq = rope(x.q[:, t0:t0 + new], at, theta)
+        mag = lambda z: z.double().abs().amax(-1, keepdim=True) * 2  # noqa: E731
+        got = q_rot[:, t0:t0 + new].double()
+        assert ((got - rq).abs() <= rq.abs() * 2 ** -8 + mag(x.q[:, t0:t0 + new]) * 2 ** -20).all()
+        rk = rope(x.k[:, t0:t0 + new], at, theta)
+        ids = torch.tensor(x.ids[b], device=x.q.device)[row // x.page]
+        gk = x.pages[:, ids, 0, :, row % x.page].double().transpose(0, 1)
+        assert ((gk - rk).abs() <= rk.abs() * 2 ** -8 + mag(x.k[:, t0:t0 + new]) * 2 ** -20).all()
+        gv = x.pages[:, ids, 1, :, row % x.page].transpose(0, 1)
+        assert torch.equal(gv, x.v[:, t0:t0 + new].to(torch.bfloat16))
+        want[:, ids, 0, :, row % x.page] = gk.transpose(0, 1)
+        want[:, ids, 1, :, row % x.page] = gv.double().transpose(0, 1)
+    got = x.pages.double()  # every other slot is as it was (NaN or an earlier row)
+    assert torch.equal(got.nan_to_num(123.0), want.nan_to_num(123.0))
+
+
+@pytest.mark.parametrize("new,past,L,H,G,page,pad,lead", [
+    ([1], [0], 1, 1, 1, 16, 0, 0),
+    ([1], [383], 18, 8, 4, 64, 0, 0),
+    ([1] * 33, list(range(33)), 2, 2, 8, 16, 0, 0),
+    ([1, 0, 17, 64, 3, 0], [5, 9, 0, 15, 63, 0], 2, 4, 2, 32, 5, 3),
+    ([130, 1, 257], [7, 200, 0], 1, 16, 1, 128, 2, 0),
+    ([5] * 70, [250] * 70, 1, 2, 4, 256, 0, 1),
+])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append(new, past, L, H, G, page, pad, lead, dtype):
+    x = Batch(new, past, L=L, H=H, G=G, page=page, pad=pad, lead=lead, dtype=dtype, seed=1)
+    off = torch.arange(x.B, dtype=torch.int32, device="cuda") * 37
+    before, q_rot = x.pages.clone(), torch.full_like(x.out, 7.0)
+    assert x.call_append(msa, off, 16, q_rot=q_rot) == 1
+    _check_append(x, q_rot, before, off, 16)
+    own = torch.zeros(x.T, dtype=torch.bool)
+    own[lead:lead + sum(new)] = True
+    assert (q_rot[:, ~own.cuda()] == 7.0).all()
+    assert x.err.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_from_a_fused_projection_at_far_positions(dtype):
+    x = Batch([3, 40, 1], [100, 0, 31], L=2, H=2, G=4, page=16, pad=2, seed=2, dtype=dtype)
+    w = torch.randn((2, x.T, x.HQ + 2 * x.H, D), device="cuda").to(dtype)
+    x.q, x.k, x.v = w[:, :, :x.HQ], w[:, :, x.HQ:x.HQ + x.H], w[:, :, x.HQ + x.H:]
+    before, q_rot = x.pages.clone(), torch.full_like(x.out, 7.0)
+    stride = w.stride(1)
+    x.call_append(msa, None, 2_000_000_000, theta=5e5, q_rot=q_rot, q_stride=stride, k_stride=stride, v_stride=stride)
+    _check_append(x, q_rot, before, None, 2_000_000_000, 5e5)
+
+
+def test_append_without_queries_and_twice():
+    x = Batch([4, 9], [2, 0], L=2, H=4, G=2, page=16, seed=3)
+    before, q = x.pages.clone(), x.q
+    x.q = None
+    x.call_append(msa)
+    first = x.pages.clone()
+    x.call_append(msa)  # lengths are not advanced: the same rows again
+    assert torch.equal(first.view(torch.int16), x.pages.view(torch.int16))
+    x.q = q
+    q_rot = torch.empty_like(x.out)
+    x.call_append(msa, q_rot=q_rot)
+    assert torch.equal(first.view(torch.int16), x.pages.view(torch.int16))
+    _check_append(x, q_rot, before, None, 16)
+
+
+def test_append_device_conditions():
+    x = Batch([4, 4, 4, 4], [14, 0, 3, 2], L=2, H=2, G=2, page=16, seed=4)
+    ok = Batch([4, 4, 4, 4], [14, 0, 3, 2], L=2, H=2, G=2, page=16, seed=4)
+    q_rot = torch.full_like(x.out, 7.0)
+    ok.call_append(msa, q_rot=torch.empty_like(q_rot))
+    x.seq_len[0] = x.max_pages * x.page + 2  # the last two of four rows do not fit
+    for p in range(2, x.max_pages):  # (its table: real pages throughout)
+        x.table[0, p] = x.n_pages - 1
+    x.table[1, 0] = x.n_pages                # a page that does not exist
+    x.seq_len[2] = 3                         # fewer rows than new tokens
+    x.call_append(msa, q_rot=q_rot)
+    assert x.err.item() == msa.MSA_DEVERR_LOCAL_FULL | msa.MSA_DEVERR_BAD_PAGE | msa.MSA_DEVERR_BAD_OFFSETS
+    ids3 = x.ids[3][0]  # the last sequence is unaffected
+    assert torch.equal(x.pages[:, ids3].view(torch.int16), ok.pages[:, ids3].view(torch.int16))
+    x.err.zero_()
+    x.off[2] = 9999  # sequences 1 and 2 unusable
+    x.call_append(msa, q_rot=q_rot)
+    assert x.err.item() & msa.MSA_DEVERR_BAD_OFFSETS
+
+
+# ----------------------------------------------------------------------------- attend
+
+CASES = {
+    "one row": dict(new=[1], past=[0]),
+    "one token, nothing before": dict(new=[1], past=[0], H=8, G=4, groups=[0, 1], mem=[0]),
+    "one long sequence": dict(new=[1], past=[5000], H=1, G=8, page=64),
+    "tile edges": dict(new=[1] * 8, past=[14, 15, 16, 17, 30, 31, 32, 63], groups=[0, 3, 8], mem=[16, 33]),
+    "ragged groups": dict(new=[1] * 9, past=[0, 400, 3, 77, 150, 31, 8, 250, 1], L=3, H=2, G=4, page=32,
+                          groups=[0, 4, 5, 8], mem=[[100, 0, 257], [1, 2, 3], [700, 64, 65]], pad=3, lead=2),
+    "one query head": dict(new=[1] * 5, past=[20, 100, 3, 0, 64], H=4, G=1, groups=[0, 5], mem=[300]),
+    "two query heads": dict(new=[1, 0, 2, 0], past=[20, 4, 3, 0], H=3, G=2, groups=[0, 4], mem=[129]),
+    "drafts": dict(new=[5] * 7, past=[0, 1, 11, 12, 100, 250, 31], L=2, H=2, G=4, groups=[0, 7], mem=[200]),
+    "wide drafts": dict(new=[3] * 6, past=[0, 13, 14, 15, 90, 41], H=2, G=8, groups=[0, 2, 6], mem=[5, 64]),
+    "many tokens": dict(new=[70, 1, 33, 0, 129], past=[0, 300, 64, 5, 13], H=2, G=4, page=64, groups=[0, 4],
+                        mem=[150], pad=1),
+    "many tokens alone": dict(new=[100, 90], past=[0, 31], H=1, G=2, page=128),
+    "questions": dict(new=[128, 200, 97], past=[0, 0, 50], H=1, G=4, page=16, groups=[0, 3], mem=[256]),
+    "long memory": dict(new=[1] * 40, past=[i * 5 for i in range(40)], H=1, G=4, page=16, groups=[0, 38, 40],
+                        mem=[4100, 130]),
+    "sixteen key heads": dict(new=[1] * 3, past=[10, 20, 30], H=16, G=2, groups=[0, 3], mem=[70]),
+    "peaked": dict(new=[1, 2, 20], past=[50, 60, 70], H=2, G=4, groups=[0, 3], mem=[300], scale=8.0),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_attend(name):
+    x = Batch(seed=5, **CASES[name])
+    x.call_attend(msa)
+    x.check()
+    assert x.err.item() == 0
+    first = x.out.clone()
+    x.call_attend(msa)  # the workspace is ready again, and the order of arrival changes nothing
+    assert torch.equal(first.view(torch.int16), x.out.view(torch.int16))
+
+
+def test_one_workspace_for_calls_of_other_sizes():
+    a = Batch([1] * 3, [2000, 7, 900], H=2, G=4, groups=[0, 3], mem=[40], seed=6)
+    b = Batch([1], [700], H=1, G=8, page=64, seed=7)
+    c = Batch([60, 50], [0, 20], H=2, G=4, groups=[0, 2], mem=[300], seed=8)
+    need = max(msa.msa_shared_attend_workspace_size(x.T, x.B, x.NG, x.L, x.HQ, x.H) for x in (a, b, c))
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    a.ws = b.ws = c.ws = ws
+    for x in (a, b, c, b, a, c):
+        x.out.fill_(7.0)
+        x.call_attend(msa)
+        x.check()
+
+
+def test_rows_that_see_nothing_are_zero():
+    x = Batch([3, 2, 1], [0, 0, 0], H=2, G=4, groups=[1, 2], mem=[20], seed=9)
+    x.seq_len[0], x.seq_len[1] = 1, 0  # fewer stored rows than new tokens: the first tokens see none
+    x.call_attend(msa)
+    x.check()
+    assert (x.out[:, :2] == 0).all() and (x.out[:, 2] != 0).any()
+
+
+@pytest.mark.parametrize("G,new", [(4, 4), (8, 3), (1, 16), (2, 40), (4, 150)])
+def test_values_that_are_not_finite_stay_behind_the_causal_limit(G, new):
+    x = Batch([new, 2], [21, 3], H=1, G=G, groups=[0, 2], mem=[18], seed=10)
+    last = x.ids[0][(21 + new - 1) // 16], (21 + new - 1) % 16
+    x.pages[:, last[0], 1, :, last[1]] = float("inf")
+    x.pages[:, last[0], 0, :, last[1]] = float("nan")
+    x.call_attend(msa)
+    got = x.out.clone()
+    assert got[:, new - 1].isnan().all()  # the last token sees its own row
+    x.pages[:, last[0], :, :, last[1]] = 0.0
+    x.call_attend(msa)
+    assert torch.equal(got[:, :new - 1].view(torch.int16), x.out[:, :new - 1].view(torch.int16))
+    assert torch.equal(got[:, new:].view(torch.int16), x.out[:, new:].view(torch.int16))
+    x.check()
+
+
+def test_attend_device_conditions():
+    x = Batch([1, 1, 1, 1], [40, 40, 40, 40], H=2, G=4, groups=[0, 2, 4], mem=[30, 50], seed=11)
+    good = x.table.clone()
+    x.table[1, 1] = -1                          # rows 16..31 of sequence 1 are not seen
+    x.mem_len[1, 0] = 60                        # clamped to 50
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_PAGE | msa.MSA_DEVERR_CAPACITY
+    want, tol = x.attend()
+    for b in (0, 2, 3):
+        assert ((x.out[:, b].double() - want[:, b]).abs() <= tol[:, b]).all()
+    loc = x.rows(1, 41)
+    keep = torch.tensor([i for i in range(41) if not 16 <= i < 32], device="cuda")
+    k = torch.cat([x.mem[0, 0, 0, :, :30].double(), loc[0, 0][:, keep]], 1)
+    v = torch.cat([x.mem[0, 0, 1, :, :30].double(), loc[1, 0][:, keep]], 1)
+    s = torch.einsum("hgd,hkd->hgk", x.q[0, 1].double().view(2, 4, D), k) * D ** -0.5
+    w = torch.einsum("hgk,hkd->hgd", torch.softmax(s, -1), v).reshape(8, D)
+    assert ((x.out[0, 1].double() - w).abs() <= tol[0, 1] + 2 ** -7 * w.abs()).all()
+    x.table.copy_(good)
+    x.mem_len[1, 0] = 50
+    x.err.zero_()
+    x.off[2] = 4000                             # sequences 1 and 2 unusable: left as they were
+    x.out.fill_(7.0)
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_OFFSETS
+    assert (x.out[:, 1:3] == 7.0).all()
+    for b in (0, 3):
+        assert ((x.out[:, b].double() - want[:, b]).abs() <= tol[:, b]).all()
+    x.off[2] = 2
+    x.err.zero_()
+    x.goff[1] = -5                              # both groups unusable: no memory
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_OFFSETS
+    x.goff[1] = 2
+    x.NG, x.err[0] = 0, 0
+    x.check()
+    x.seq_len[0] = 10_000                       # past the table: clamped to its 64 rows
+    x.table[0, 3] = x.ids[0][0]
+    x.ids[0] = x.ids[0] + [x.ids[0][0]]
+    x.pages.nan_to_num_(0.25)
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_LOCAL_FULL
+    x.check()
+
+
+def test_offsets_past_32_bits():
+    # a pool of more than 2^31 elements; the sequence's rows lie in its last pages
+    H, page = 8, 64
+    n_pages = (2 ** 31) // (2 * H * page * D) + 40
+    x = Batch([1, 2], [300, 70], H=H, G=4, page=page, groups=[0, 2], mem=[30], seed=12)
+    big = torch.empty((1, n_pages, 2, H, page, D), dtype=torch.bfloat16, device="cuda")
+    big[:, -x.n_pages:] = x.pages
+    shift = n_pages - x.n_pages
+    x.pages, x.n_pages = big, n_pages
+    x.ids = [[i + shift for i in r] for r in x.ids]
+    x.table += shift * (x.table < 0x7FFFFFF0).int()
+    before, q_rot = big[:, shift:].clone(), torch.empty_like(x.out)
+    x.call_append(msa, q_rot=q_rot)
+    x.q = q_rot
+    x.call_attend(msa)
+    x.check()
+    assert not torch.equal(before.view(torch.int16), big[:, shift:].view(torch.int16))
+    assert x.err.item() == 0
+
+
+def test_append_then_attend_captured_and_replayed_on_its_own_stream():
+    x = Batch([1, 1, 1], [30, 0, 200], L=2, H=2, G=4, groups=[0, 3], mem=[100], seed=13)
+    q_rot, s = torch.empty_like(x.out), torch.cuda.Stream()
+    raw = x.q
+    x.call_attend(msa)  # (allocates the workspace)
+
+    def step():
+        x.q = raw
+        x.call_append(msa, q_rot=q_rot, stream=s)
+        x.q = q_rot
+        x.call_attend(msa, stream=s)
+
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for _ in range(3):  # the replays read the lengths of the moment
+        x.seq_len += 1
+        x.past = [p + 1 for p in x.past]
+        for b in range(3):
+            need = -(-(x.past[b] + 1) // x.page)
+            if need > len(x.ids[b]):  # a spare page
+                x.ids[b].append([i for i in range(x.n_pages) if all(i not in r for r in x.ids)][0])
+                x.table[b, need - 1] = x.ids[b][-1]
+        raw.normal_()
+        x.k.normal_()
+        graph.replay()
+        torch.cuda.synchronize()
+        x.check()
+    assert x.err.item() == 0
+
+
+def test_agrees_with_the_single_query_decode_step():
+    # one sequence, one group: msa_sparse_decode of the same query, memory and local rows
+    L, H, G, M, n = 3, 8, 4, 120, 77
+    x = Batch([1], [n], L=L, H=H, G=G, page=32, groups=[0, 1], mem=[[120, 64, 9]], M=M, seed=14)
+    loc = x.rows(0, n).to(torch.bfloat16)
+    local = [torch.zeros((1, L, H, 128, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for c, src in zip(local, loc):
+        c[0, :, :, :n] = src
+    out = torch.empty((1, L, H * G, D), dtype=torch.bfloat16, device="cuda")
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(msa.msa_sparse_decode_workspace_size(1, L, H * G, H), dtype=torch.uint8, device="cuda")
+    mem = x.mem.nan_to_num(0.0)
+    msa.msa_sparse_decode(x.q[:, 0].contiguous(), x.k[:, 0].contiguous(), x.v[:, 0].contiguous(), 1, L, H * G, H, D,
+                          local[0], local[1], ln, 128, mem, x.mem_len, M, 16, 1e6, D ** -0.5, out, ws)
+    q_rot = torch.empty_like(x.out)
+    x.call_append(msa, q_rot=q_rot)
+    x.q = q_rot
+    x.call_attend(msa)
+    x.check()
+    assert torch.equal(x.rows(0, n + 1)[0, :, :, n].to(torch.bfloat16), local[0][0, :, :, n])
+    # the two differ by the rounding of the rotated query to bf16 and the two outputs' own
+    a, b = x.out[:, 0].double(), out[0].double()
+    assert (a - b).norm() / b.norm() <= 2 ** -7

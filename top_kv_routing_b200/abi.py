@@ -1,4 +1,4 @@
-"""Thin ctypes binding over the six C-ABI libraries in ``lib/`` (see ``include/*.h``).
+"""Thin ctypes binding over the seven C-ABI libraries in ``lib/`` (see ``include/*.h``).
 
 Argument marshalling only; every step runs in the libraries' CUDA kernels.  PyTorch is
 used by callers for device memory and streams.  There is no CPU fallback: importing this
@@ -20,7 +20,7 @@ MSA_ROUTE_AUTO, MSA_ROUTE_SCAN, MSA_ROUTE_TENSOR, MSA_ROUTE_TENSOR_F8 = 0, 1, 2,
 MSA_ROUTE_LAYER_MEAN = 16  # OR-ed with a path: one selection for all layers
 MSA_ROUTE_FILTER_SCORES = 32  # OR-ed with a tensor path: the filter's own top-k and scores
 (MSA_DEVERR_CAPACITY, MSA_DEVERR_BAD_DOC, MSA_DEVERR_LOCAL_FULL, MSA_DEVERR_BAD_OFFSETS, MSA_DEVERR_TIMEOUT,
- MSA_DEVERR_UNCERTIFIED) = 1, 2, 4, 8, 16, 32
+ MSA_DEVERR_UNCERTIFIED, MSA_DEVERR_BAD_PAGE) = 1, 2, 4, 8, 16, 32, 64
 
 _STATUS = {1: "MSA_ERR_INVALID_ARG", 2: "MSA_ERR_UNSUPPORTED", 3: "MSA_ERR_CUDA", 4: "MSA_ERR_CAPACITY",
            5: "MSA_ERR_TIMEOUT", 6: "MSA_ERR_IO"}
@@ -48,6 +48,7 @@ gather_lib = _load("gather")
 decode_lib = _load("decode")
 prefill_lib = _load("prefill")
 bank_lib = _load("bank")
+paged_lib = _load("paged")
 
 pool_lib.msa_count_chunks.argtypes = [_p, _i32, _i32, _p]
 pool_lib.msa_count_chunks.restype = _i64
@@ -118,6 +119,19 @@ bank_lib.msa_bank_append_offsets.argtypes = [_p, _i64, _p, _i64, _p]
 bank_lib.msa_bank_append_offsets.restype = _i32
 bank_lib.msa_bank_last_error.restype = ctypes.c_char_p
 
+paged_lib.msa_paged_append.argtypes = [_p, _p, _p, _i32, _i64, _i64, _i64, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p,
+                                       _i32, _i32, _p, _i32, _p, _p, _i32, _f32, _p, _p, _p]
+paged_lib.msa_paged_append.restype = _i32
+paged_lib.msa_shared_attend_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)]
+paged_lib.msa_shared_attend_workspace_size.restype = _i32
+paged_lib.msa_shared_attend.argtypes = [_p, _p, _i32, _i32, _i32, _i32, _i32, _i32, _p, _p, _i32, _p, _i32, _p, _i32,
+                                        _i32, _p, _i32, _p, _f32, _p, _p, _sz, _p, _p]
+paged_lib.msa_shared_attend.restype = _i32
+paged_lib.msa_paged_last_launch_count.argtypes = []
+paged_lib.msa_paged_last_launch_count.restype = _i32
+paged_lib.msa_paged_last_error.restype = ctypes.c_char_p
+MSA_PAGED_MAX_SEQS = 1024
+
 # Kernel launches enqueued by each entry point (the route count is read back per call).
 LAUNCHES_POOL = 1
 LAUNCHES_GATHER = 1
@@ -126,7 +140,7 @@ LAUNCHES_PREFILL = 3
 
 
 def loaded_libraries() -> list[str]:
-    return [os.path.join(LIB_DIR, f"libmsa_{n}.so") for n in ("pool", "route", "gather", "decode", "prefill", "bank")]
+    return [os.path.join(LIB_DIR, f"libmsa_{n}.so") for n in ("pool", "route", "gather", "decode", "prefill", "bank", "paged")]
 
 
 def _ptr(t) -> int | None:
@@ -322,6 +336,52 @@ def msa_sparse_prefill(q, k_new, v_new, n_new: int, n_queries: int, n_layers: in
                                         local_cap, _ptr(mem_kv), _ptr(mem_len), max_mem_chunks, rope_pos_offset,
                                         rope_theta, softmax_scale, _ptr(out), _ptr(dev_err), _stream(stream))
     _check(st, "msa_sparse_prefill", prefill_lib, "msa_prefill_last_error")
+
+
+# ----------------------------------------------------------------------------- paged batches
+
+def msa_paged_append(q, k_new, v_new, q_offsets, n_tokens: int, n_seqs: int, n_layers: int, n_q_heads: int,
+                     n_kv_heads: int, head_dim: int, kv_pages, n_pages: int, page_size: int, page_table,
+                     max_pages: int, seq_len, pos_offset, rope_pos_offset: int, rope_theta: float, q_rot,
+                     dev_err=None, in_dtype: int | None = None, q_stride: int = 0, k_stride: int = 0,
+                     v_stride: int = 0, stream=None) -> int:
+    """Rotates and stores the new tokens' keys and values in their sequences' pages and rotates
+    the queries into q_rot (include/msa_paged.h).  q and q_rot may both be None; strides are
+    elements from one token to the next, 0 for dense rows.  Returns the kernels enqueued."""
+    if in_dtype is None:
+        in_dtype = MSA_BF16 if str(k_new.dtype) == "torch.bfloat16" else MSA_F32
+    st = paged_lib.msa_paged_append(_ptr(q), _ptr(k_new), _ptr(v_new), in_dtype, q_stride, k_stride, v_stride,
+                                    _ptr(q_offsets), n_tokens, n_seqs, n_layers, n_q_heads, n_kv_heads, head_dim,
+                                    _ptr(kv_pages), n_pages, page_size, _ptr(page_table), max_pages, _ptr(seq_len),
+                                    _ptr(pos_offset), rope_pos_offset, rope_theta, _ptr(q_rot), _ptr(dev_err),
+                                    _stream(stream))
+    _check(st, "msa_paged_append", paged_lib, "msa_paged_last_error")
+    return int(paged_lib.msa_paged_last_launch_count())
+
+
+def msa_shared_attend_workspace_size(n_tokens: int, n_seqs: int, n_groups: int, n_layers: int, n_q_heads: int,
+                                     n_kv_heads: int) -> int:
+    out = _sz(0)
+    st = paged_lib.msa_shared_attend_workspace_size(n_tokens, n_seqs, n_groups, n_layers, n_q_heads, n_kv_heads,
+                                                    ctypes.byref(out))
+    _check(st, "msa_shared_attend_workspace_size", paged_lib, "msa_paged_last_error")
+    return int(out.value)
+
+
+def msa_shared_attend(q, q_offsets, n_tokens: int, n_seqs: int, n_layers: int, n_q_heads: int, n_kv_heads: int,
+                      head_dim: int, mem_kv, mem_len, max_mem_chunks: int, group_offsets, n_groups: int, kv_pages,
+                      n_pages: int, page_size: int, page_table, max_pages: int, seq_len, softmax_scale: float, out,
+                      workspace, dev_err=None, stream=None) -> int:
+    """Every new token over its group's memory (computed once for the group's sequences) and its
+    own sequence's pages, causal over the new tokens (include/msa_paged.h).  Returns the kernels
+    enqueued."""
+    st = paged_lib.msa_shared_attend(_ptr(q), _ptr(q_offsets), n_tokens, n_seqs, n_layers, n_q_heads, n_kv_heads,
+                                     head_dim, _ptr(mem_kv), _ptr(mem_len), max_mem_chunks, _ptr(group_offsets),
+                                     n_groups, _ptr(kv_pages), n_pages, page_size, _ptr(page_table), max_pages,
+                                     _ptr(seq_len), softmax_scale, _ptr(out), _ptr(workspace), _nbytes(workspace),
+                                     _ptr(dev_err), _stream(stream))
+    _check(st, "msa_shared_attend", paged_lib, "msa_paged_last_error")
+    return int(paged_lib.msa_paged_last_launch_count())
 
 
 # ----------------------------------------------------------------------------- bank files

@@ -1,4 +1,4 @@
-"""Builds the four C-ABI libraries (and the synthetic-input device library) for sm_100a.
+"""Builds the C-ABI libraries (and the synthetic-input device library) for sm_100a.
 
 Run ``python top_kv_routing_b200/build.py``; the shared objects land in-tree under
 ``top_kv_routing_b200/lib`` and ``msa_synth/`` so they travel with the source tree.
@@ -29,12 +29,13 @@ TARGETS = {
     os.path.join(LIB, "libmsa_decode.so"): ["decode.cu"],
     os.path.join(LIB, "libmsa_prefill.so"): ["prefill.cu", "prefill_tc.cu"],
     os.path.join(LIB, "libmsa_bank.so"): ["bank.cu"],
+    os.path.join(LIB, "libmsa_paged.so"): ["paged.cu", "paged_rows.cu"],
 }
 SYNTH_TARGET = os.path.join(SYNTH, "libmsa_synth.so")
 
 LIBRARIES = {"pool": "libmsa_pool.so", "route": "libmsa_route.so", "gather": "libmsa_gather.so",
              "decode": "libmsa_decode.so", "prefill": "libmsa_prefill.so",
-             "bank": "libmsa_bank.so"}
+             "bank": "libmsa_bank.so", "paged": "libmsa_paged.so"}
 
 
 def nvcc() -> str:

@@ -1,0 +1,71 @@
+// Paged batches (host-side interfaces between paged.cu and its kernels, and the device
+// helpers they share; not part of the ABI).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+#include "msa_paged.h"
+
+namespace paged {
+
+constexpr int kD = 128;
+constexpr int kMaxSeqs = MSA_PAGED_MAX_SEQS;
+
+// Arguments of one msa_shared_attend call, checked.
+struct Attend {
+  const __nv_bfloat16* q;          // [L][T][H*G][128]
+  __nv_bfloat16* out;              // [L][T][H*G][128]
+  const int32_t* q_offsets;        // [B + 1]
+  const int32_t* seq_len;          // [B]
+  const int32_t* group_offsets;    // [NG + 1]
+  const __nv_bfloat16* mem_kv;     // [NG][L][2][H][M_max][128]
+  const int32_t* mem_len;          // [NG][L]
+  const __nv_bfloat16* pages;      // [L][NP][2][H][page][128]
+  const int32_t* page_table;       // [B][max_pages]
+  int T, B, NG, L, H, G, M_max, NP, log2_page, max_pages;
+  float qscale;                    // softmax scale x log2(e)
+  unsigned char* ws;
+  int32_t* dev_err;
+};
+
+// ---- the row kernel (paged_rows.cu): 8 or 16 rows of one sequence per warp, mma.sync
+constexpr int kRowWarps = 8;       // warps per CTA
+constexpr int kRowCtas = 160;      // CTAs the workspace is laid out for (one per SM)
+constexpr int kRowWorkers = kRowCtas * kRowWarps;
+
+// Workspace: arrival counters (zero between calls, at the same place for every size), then
+// two piece slots per worker.
+constexpr size_t kWsCounters = 0;
+constexpr size_t kWsStat = kRowWorkers * sizeof(int32_t);
+constexpr size_t kWsPart = kWsStat + (size_t)2 * kRowWorkers * 16 * sizeof(float2);
+constexpr size_t kWsEnd = kWsPart + (size_t)2 * kRowWorkers * 16 * kD * sizeof(float);
+
+cudaError_t launch_rows(const Attend& a, cudaStream_t s);
+
+// ---- device helpers
+
+// 2^x by the hardware approximation (relative error about 2^-22, 2^-inf = 0).
+__device__ __forceinline__ float ex2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Launched as a programmatic dependent: nothing an earlier kernel writes is read before this.
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// The tokens [lo, lo + n) of sequence b; n = 0 and false where the offsets are unusable.
+__device__ __forceinline__ bool sequence_tokens(const int32_t* __restrict__ off, int b, int T, int& lo, int& n) {
+  lo = off[b];
+  const int hi = off[b + 1];
+  const bool ok = lo >= 0 && hi >= lo && hi <= T;
+  n = ok ? hi - lo : 0;
+  return ok;
+}
+
+}  // namespace paged
