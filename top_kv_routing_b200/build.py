@@ -29,7 +29,7 @@ TARGETS = {
     os.path.join(LIB, "libmsa_decode.so"): ["decode.cu"],
     os.path.join(LIB, "libmsa_prefill.so"): ["prefill.cu", "prefill_tc.cu"],
     os.path.join(LIB, "libmsa_bank.so"): ["bank.cu"],
-    os.path.join(LIB, "libmsa_paged.so"): ["paged.cu", "paged_rows.cu"],
+    os.path.join(LIB, "libmsa_paged.so"): ["paged.cu", "paged_rows.cu", "paged_tc.cu"],
 }
 SYNTH_TARGET = os.path.join(SYNTH, "libmsa_synth.so")
 

@@ -19,6 +19,7 @@ using namespace paged;
 
 constexpr int kHalf = 64;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSharedRows = 16;
 
 static thread_local int32_t g_launches = 0;
 
@@ -355,7 +356,8 @@ extern "C" msa_status msa_shared_attend_workspace_size(int32_t n_tokens, int32_t
   if (st == MSA_OK) st = check_batch(n_tokens, n_seqs, n_layers);
   if (st != MSA_OK) return st;
   if (n_groups < 0 || n_groups > n_seqs) return msa_fail(MSA_ERR_INVALID_ARG, "n_groups must be in [0, n_seqs]");
-  *bytes = kWsEnd;
+  const int64_t rows = (int64_t)n_layers * n_tokens * n_q_heads;
+  *bytes = kWsEnd + (n_groups > 0 ? memory_bytes(rows, memory_splits(rows)) : 0);
   return msa_ok();
 }
 
@@ -409,8 +411,19 @@ extern "C" msa_status msa_shared_attend(const void* q, const int32_t* q_offsets,
   a.qscale = softmax_scale * kLog2e;
   a.ws = static_cast<unsigned char*>(workspace);
   a.dev_err = dev_err;
-  MSA_CUDA_TRY(launch_rows(a, reinterpret_cast<cudaStream_t>(stream)));
-  g_launches = 1;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // The memory once for a whole group, on the tensor cores, where its sequences share enough
+  // rows; a group of one or two answers reads it sooner within the row kernel.
+  const int64_t rows = (int64_t)n_layers * n_tokens * n_q_heads;
+  const bool shared = n_groups > 0 && (int64_t)n_tokens * a.G > (int64_t)kSharedRows * n_groups;
+  const int splits = shared ? memory_splits(rows) : 0;
+  if (shared) {
+    if ((int64_t)n_groups * n_layers * 2 * n_kv_heads * max_mem_chunks + 128 > 0x7fffffffll)
+      return msa_fail(MSA_ERR_CAPACITY, "mem_kv beyond 2^31 rows of 128 elements");
+    MSA_CUDA_TRY(launch_memory(a, splits, s));
+  }
+  MSA_CUDA_TRY(launch_rows(a, splits, s));
+  g_launches = shared ? 2 : 1;
   return msa_ok();
 }
 

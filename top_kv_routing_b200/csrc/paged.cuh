@@ -38,11 +38,33 @@ constexpr int kRowWorkers = kRowCtas * kRowWarps;
 // Workspace: arrival counters (zero between calls, at the same place for every size), then
 // two piece slots per worker.
 constexpr size_t kWsCounters = 0;
-constexpr size_t kWsStat = kRowWorkers * sizeof(int32_t);
+constexpr size_t kWsSplits = kRowWorkers * sizeof(int32_t);  // key splits that the memory kernel chose
+constexpr size_t kWsStat = kWsSplits + 128;
 constexpr size_t kWsPart = kWsStat + (size_t)2 * kRowWorkers * 16 * sizeof(float2);
 constexpr size_t kWsEnd = kWsPart + (size_t)2 * kRowWorkers * 16 * kD * sizeof(float);
 
-cudaError_t launch_rows(const Attend& a, cudaStream_t s);
+// memory_splits > 0: the memory part was computed by the memory kernel (with at most that many
+// key splits), otherwise the row kernel walks the memory itself.
+cudaError_t launch_rows(const Attend& a, int memory_splits, cudaStream_t s);
+
+// ---- the memory kernel (paged_tc.cu): all rows of a group at once, tcgen05.  Its output, per
+// partial slot and row (layer, token, query head): the unnormalised output, then (after all
+// of them) the row's maximum (log2 domain) and sum.  A group of at most one row tile (128 / G
+// tokens) has 2 x splits slots, others `splits`.
+constexpr size_t kWsMemory = kWsEnd;
+// Rows x splits are bounded by what two waves of one pair of row tiles per SM hold.
+constexpr int64_t kSplitRows = 2 * 148 * 256;
+constexpr int kMaxSplits = 64;
+inline int memory_splits(int64_t rows) {
+  return (int)(rows >= kSplitRows ? 1 : kSplitRows / rows < kMaxSplits ? kSplitRows / rows : kMaxSplits);
+}
+__host__ __device__ inline size_t memory_part_bytes(int64_t rows, int splits) {
+  return (size_t)rows * 2 * splits * kD * sizeof(float);
+}
+inline size_t memory_bytes(int64_t rows, int splits) {
+  return memory_part_bytes(rows, splits) + (size_t)rows * 2 * splits * sizeof(float2);
+}
+cudaError_t launch_memory(const Attend& a, int max_splits, cudaStream_t s);
 
 // ---- device helpers
 
@@ -64,6 +86,27 @@ __device__ __forceinline__ bool sequence_tokens(const int32_t* __restrict__ off,
   lo = off[b];
   const int hi = off[b + 1];
   const bool ok = lo >= 0 && hi >= lo && hi <= T;
+  n = ok ? hi - lo : 0;
+  return ok;
+}
+
+// Whether the group offsets are non-decreasing within [0, B] (all threads of the block call it
+// and get the same answer).
+__device__ __forceinline__ bool group_offsets_usable(const Attend& a, int tid, int threads) {
+  bool ok = true;
+  for (int g = tid; g < a.NG; g += threads) {
+    const int s = a.group_offsets[g], e = a.group_offsets[g + 1];
+    ok &= s >= 0 && e >= s && e <= a.B;
+  }
+  return __syncthreads_and(ok);
+}
+
+// The packed tokens [lo, lo + n) of group g (whose offsets are usable); false where the
+// sequences' offsets are not.
+__device__ __forceinline__ bool group_tokens(const Attend& a, int g, int& lo, int& n) {
+  lo = a.q_offsets[a.group_offsets[g]];
+  const int hi = a.q_offsets[a.group_offsets[g + 1]];
+  const bool ok = lo >= 0 && hi >= lo && hi <= a.T;
   n = ok ? hi - lo : 0;
   return ok;
 }

@@ -49,7 +49,7 @@ struct Tables {
   int len[kMaxSeqs];           // rows with the new tokens, as given
   int grp[kMaxSeqs];           // group, or -1
   int mt[kMaxSeqs];            // memory tiles (the longest layer's)
-  int gmt[kMaxSeqs];           // the same by group
+  int gmt[kMaxSeqs];           // the same by group (PART: partial slots per split)
   int64_t warp_sum[kRowWarps];
 };
 
@@ -69,8 +69,10 @@ __device__ __forceinline__ bool not_finite(uint32_t st, int lane) {
   return bad;
 }
 
-template <int G, int NR>
-__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ Attend a) {
+// PART: the memory part comes from the memory kernel's partial results.
+template <int G, int NR, bool PART>
+__global__ void __launch_bounds__(kThreads, 1)
+    rows_kernel(const __grid_constant__ Attend a, int max_splits) {
   constexpr int R = 8 * NR;       // rows of a unit
   constexpr int kTok = R / G;     // tokens of a unit
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -81,7 +83,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
   const int page_mask = (1 << a.log2_page) - 1;
   const int64_t cap = (int64_t)a.max_pages << a.log2_page;
 
-  wait_for_earlier_kernels();
+  // With PART this kernel follows the memory kernel, which lets it start once every one of its
+  // CTAs has seen all earlier kernels complete: only the memory kernel itself is still to be
+  // waited for, before its results are read (and before this kernel ends, so that whoever
+  // waits for this one has waited for both).
+  if (!PART) wait_for_earlier_kernels();
   let_next_kernel_start();
 
   // ---- tables
@@ -97,29 +103,34 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     tb.mt[b] = 0;
   }
   __syncthreads();
-  for (int gr = warp; gr < a.NG; gr += kRowWarps) {
+  const bool groups_ok = group_offsets_usable(a, tid, kThreads);  // (a barrier for all threads)
+  if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+  for (int gr = warp; gr < a.NG && groups_ok; gr += kRowWarps) {
     const int s = a.group_offsets[gr], e = a.group_offsets[gr + 1];
-    if (s < 0 || e < s || e > a.B) {
-      if (blockIdx.x == 0 && lane == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-      continue;
-    }
     int most = 0;
-    for (int l = lane; l < a.L; l += 32) {
-      int m = a.mem_len[(int64_t)gr * a.L + l];
-      if (m > a.M_max) {
-        if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
-        m = a.M_max;
+    if (PART) {
+      // partial slots per split: two where the group's rows fit one row tile, none where the
+      // memory kernel left the group out
+      int lo, n;
+      if (group_tokens(a, gr, lo, n)) most = n <= 128 / G ? 2 : 1;
+      for (int b = s + lane; b < e; b += 32)
+        if (tb.tok0[b] >= lo && tb.tok0[b] + tb.n[b] <= lo + n) tb.grp[b] = gr;
+    } else {
+      for (int l = lane; l < a.L; l += 32) {
+        int m = a.mem_len[(int64_t)gr * a.L + l];
+        if (m > a.M_max) {
+          if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
+          m = a.M_max;
+        }
+        most = max(most, m);
       }
-      most = max(most, m);
+      most = (__reduce_max_sync(0xffffffffu, most) + kTileKeys - 1) / kTileKeys;
+      for (int b = s + lane; b < e; b += 32) tb.grp[b] = gr;
     }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) tb.gmt[gr] = (most + kTileKeys - 1) / kTileKeys;
-    // (the highest group where unusable offsets make groups overlap: every CTA has to cut the
-    // same line)
-    for (int b = s + lane; b < e; b += 32) atomicMax(&tb.grp[b], gr);
+    if (lane == 0) tb.gmt[gr] = most;
   }
   __syncthreads();
-  for (int b = tid; b < a.B; b += kThreads) tb.mt[b] = tb.grp[b] < 0 ? 0 : tb.gmt[tb.grp[b]];
+  for (int b = tid; b < a.B; b += kThreads) tb.mt[b] = PART || tb.grp[b] < 0 ? 0 : tb.gmt[tb.grp[b]];
   __syncthreads();
   // tiles of sequence b per (layer, key head): row tiles x key tiles (at least one, so that a
   // unit without any key still writes its zeros)
@@ -162,7 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
   const int64_t total = tb.scan[a.B] * LH;
   const int64_t per = max((int64_t)kMinTiles, (total + workers - 1) / workers);
   const int64_t w0 = worker * per, w1 = min(total, w0 + per);
-  if (w0 >= w1) return;
+  if (w0 >= w1) {
+    if (PART) wait_for_earlier_kernels();
+    return;
+  }
 
   struct Cursor {
     int b, lh, rt, j;       // sequence, layer x H + key head, row tile, key tile
@@ -174,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     c.l = c.lh / a.H;
     c.h = c.lh - c.l * a.H;
     c.M = 0;
-    if (c.mt > 0) c.M = max(0, min(a.M_max, a.mem_len[(int64_t)tb.grp[c.b] * a.L + c.l]));
+    if (!PART && c.mt > 0) c.M = max(0, min(a.M_max, a.mem_len[(int64_t)tb.grp[c.b] * a.L + c.l]));
   };
   auto set_sequence = [&](Cursor& c) {
     c.RT = row_tiles(c.b);
@@ -229,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     const __nv_bfloat16 *kp, *vp;
     int rows;
     bad &= ~(1u << stage);
-    if (pc.j < pc.mt) {
+    if (!PART && pc.j < pc.mt) {
       const int64_t at = (((int64_t)tb.grp[pc.b] * a.L + pc.l) * 2 * a.H + pc.h) * a.M_max + pc.j * kTileKeys;
       kp = a.mem_kv + at * kD;
       vp = kp + (int64_t)a.H * a.M_max * kD;
@@ -281,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
   float o[16][4];
   float m[NR], lsum[NR];
   int lim[NR];  // the last page row that this thread's rows see
-  bool fresh = true;
+  bool fresh = true, memory_done = false;
   int64_t u0 = w0 - c.j;  // the unit's first tile on the line
 
   // a row's token within the sequence, and its place among the rows of q and out
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     __syncwarp();
     const int stage = i % kStages;
     const uint32_t st = my_ring + stage * kStageBytes;
-    const bool mem = c.j < c.mt;
+    const bool mem = !PART && c.j < c.mt;
     // keys of this tile below `top` are seen: the same for all rows of a memory tile
     const int key0 = mem ? c.j * kTileKeys : (c.j - c.mt) * kTileKeys;
     int top[NR];
@@ -521,6 +535,48 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
           }
         }
       }
+      if (PART && write && tb.grp[c.b] >= 0) {
+        // join the memory part: its slots in order, then this sequence's rows
+        if (!memory_done) {
+          wait_for_earlier_kernels();
+          memory_done = true;
+        }
+        const int slots = __ldcg(reinterpret_cast<const int*>(a.ws + kWsSplits)) * tb.gmt[tb.grp[c.b]];
+        const int64_t all_rows = (int64_t)a.L * a.T * Hq;
+        const float* part = reinterpret_cast<const float*>(a.ws + kWsMemory);
+        const float2* stat =
+            reinterpret_cast<const float2*>(a.ws + kWsMemory + memory_part_bytes(all_rows, max_splits));
+#pragma unroll
+        for (int v = 0; v < NR; ++v) {
+          const int r = g + 8 * v;
+          if (row_token(r) < tb.n[c.b]) {
+            const int64_t row = row_at(r) / kD;
+            float top = m[v];
+            for (int s = 0; s < slots; ++s) top = fmaxf(top, __ldcg(&stat[s * all_rows + row]).x);
+            const float base = top == -INFINITY ? 0.f : top;
+            const float own = ex2_ftz(m[v] - base);
+            sum[v] *= own;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) {
+              o[n][2 * v] *= own;
+              o[n][2 * v + 1] *= own;
+            }
+            for (int s = 0; s < slots; ++s) {
+              const float2 ml = __ldcg(&stat[s * all_rows + row]);
+              if (ml.y == 0.f) continue;  // (an empty split writes no output)
+              const float f = ex2_ftz(ml.x - base);
+              sum[v] = fmaf(f, ml.y, sum[v]);
+              const float* src = part + (s * all_rows + row) * kD + 2 * t;
+#pragma unroll
+              for (int n = 0; n < 16; ++n) {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(src + 8 * n));
+                o[n][2 * v] = fmaf(f, x.x, o[n][2 * v]);
+                o[n][2 * v + 1] = fmaf(f, x.y, o[n][2 * v + 1]);
+              }
+            }
+          }
+        }
+      }
       if (write) {
 #pragma unroll
         for (int v = 0; v < NR; ++v) {
@@ -546,13 +602,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     }
   }
   cp_async_wait<0>();
+  if (PART && !memory_done) wait_for_earlier_kernels();
 }
 
-template <int G, int NR>
-cudaError_t launch_rows_t(const Attend& a, cudaStream_t s) {
+template <int G, int NR, bool PART>
+cudaError_t launch_rows_t(const Attend& a, int memory_splits, cudaStream_t s) {
   constexpr int kSmem = kRingBytes + (int)sizeof(Tables);
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(rows_kernel<G, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(rows_kernel<G, NR, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min(msa::sm_count(), kRowCtas), 1, 1);
@@ -564,20 +621,26 @@ cudaError_t launch_rows_t(const Attend& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<G, NR>, a);
+  return cudaLaunchKernelEx(&cfg, rows_kernel<G, NR, PART>, a, memory_splits);
+}
+
+// Eight rows where the sequences have at most eight on average (their weights' residuals then
+// cost no MMA of their own), sixteen otherwise.
+template <int G>
+cudaError_t launch_rows_g(const Attend& a, int memory_splits, cudaStream_t s) {
+  const bool few = (int64_t)a.T * a.G <= 8 * (int64_t)a.B;
+  if (memory_splits > 0) return few ? launch_rows_t<G, 1, true>(a, memory_splits, s) : launch_rows_t<G, 2, true>(a, memory_splits, s);
+  return few ? launch_rows_t<G, 1, false>(a, 0, s) : launch_rows_t<G, 2, false>(a, 0, s);
 }
 
 }  // namespace
 
-// Eight rows where the sequences have at most eight on average (their weights' residuals then
-// cost no MMA of their own), sixteen otherwise.
-cudaError_t launch_rows(const Attend& a, cudaStream_t s) {
-  const bool few = (int64_t)a.T * a.G <= 8 * (int64_t)a.B;
+cudaError_t launch_rows(const Attend& a, int memory_splits, cudaStream_t s) {
   switch (a.G) {
-    case 1: return few ? launch_rows_t<1, 1>(a, s) : launch_rows_t<1, 2>(a, s);
-    case 2: return few ? launch_rows_t<2, 1>(a, s) : launch_rows_t<2, 2>(a, s);
-    case 4: return few ? launch_rows_t<4, 1>(a, s) : launch_rows_t<4, 2>(a, s);
-    default: return few ? launch_rows_t<8, 1>(a, s) : launch_rows_t<8, 2>(a, s);
+    case 1: return launch_rows_g<1>(a, memory_splits, s);
+    case 2: return launch_rows_g<2>(a, memory_splits, s);
+    case 4: return launch_rows_g<4>(a, memory_splits, s);
+    default: return launch_rows_g<8>(a, memory_splits, s);
   }
 }
 
