@@ -20,6 +20,25 @@ using namespace paged;
 constexpr int kHalf = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSharedRows = 16;
+constexpr int kBlockRows = 64;
+constexpr int64_t kMaxTensorRows = 0x7fffffff - 128;  // (TMA row coordinates are 32-bit)
+
+// Which kernels a batch takes, by its average rows (tokens x G) per sequence and group (the
+// split of the tokens over the sequences is known to the device alone; any split is computed
+// correctly by every form).
+struct Plan {
+  enum Form { kRowsOnly, kMemory, kBlocks } form;
+  int splits;  // memory form: most key splits
+};
+Plan plan_of(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t Hq, int64_t H) {
+  const int64_t G = Hq / H;
+  // Blocks of new tokens that fill half a row tile: memory and pages in one walk.
+  if (T * G >= kBlockRows * B) return {Plan::kBlocks, 0};
+  // The memory once for a whole group, on the tensor cores, where its sequences share enough
+  // rows; a group of one or two answers reads it sooner within the row kernel.
+  if (NG > 0 && T * G > kSharedRows * NG) return {Plan::kMemory, memory_splits(L * T * Hq)};
+  return {Plan::kRowsOnly, 0};
+}
 
 static thread_local int32_t g_launches = 0;
 
@@ -356,8 +375,9 @@ extern "C" msa_status msa_shared_attend_workspace_size(int32_t n_tokens, int32_t
   if (st == MSA_OK) st = check_batch(n_tokens, n_seqs, n_layers);
   if (st != MSA_OK) return st;
   if (n_groups < 0 || n_groups > n_seqs) return msa_fail(MSA_ERR_INVALID_ARG, "n_groups must be in [0, n_seqs]");
+  const Plan plan = plan_of(n_tokens, n_seqs, n_groups, n_layers, n_q_heads, n_kv_heads);
   const int64_t rows = (int64_t)n_layers * n_tokens * n_q_heads;
-  *bytes = kWsEnd + (n_groups > 0 ? memory_bytes(rows, memory_splits(rows)) : 0);
+  *bytes = kWsEnd + (plan.form == Plan::kMemory ? memory_bytes(rows, plan.splits) : 0);
   return msa_ok();
 }
 
@@ -412,18 +432,18 @@ extern "C" msa_status msa_shared_attend(const void* q, const int32_t* q_offsets,
   a.ws = static_cast<unsigned char*>(workspace);
   a.dev_err = dev_err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // The memory once for a whole group, on the tensor cores, where its sequences share enough
-  // rows; a group of one or two answers reads it sooner within the row kernel.
-  const int64_t rows = (int64_t)n_layers * n_tokens * n_q_heads;
-  const bool shared = n_groups > 0 && (int64_t)n_tokens * a.G > (int64_t)kSharedRows * n_groups;
-  const int splits = shared ? memory_splits(rows) : 0;
-  if (shared) {
-    if ((int64_t)n_groups * n_layers * 2 * n_kv_heads * max_mem_chunks + 128 > 0x7fffffffll)
-      return msa_fail(MSA_ERR_CAPACITY, "mem_kv beyond 2^31 rows of 128 elements");
-    MSA_CUDA_TRY(launch_memory(a, splits, s));
+  const Plan plan = plan_of(n_tokens, n_seqs, n_groups, n_layers, n_q_heads, n_kv_heads);
+  const int64_t mem_rows = (int64_t)n_groups * n_layers * 2 * n_kv_heads * a.M_max;
+  const int64_t page_rows = ((int64_t)n_layers * n_pages * 2 * n_kv_heads) << a.log2_page;
+  if (plan.form != Plan::kRowsOnly && (mem_rows > kMaxTensorRows || (plan.form == Plan::kBlocks && page_rows > kMaxTensorRows)))
+    return msa_fail(MSA_ERR_CAPACITY, "mem_kv or kv_pages beyond 2^31 rows of 128 elements");
+  if (plan.form == Plan::kBlocks) {
+    MSA_CUDA_TRY(launch_blocks(a, s));
+  } else {
+    if (plan.form == Plan::kMemory) MSA_CUDA_TRY(launch_memory(a, plan.splits, s));
+    MSA_CUDA_TRY(launch_rows(a, plan.splits, s));
   }
-  MSA_CUDA_TRY(launch_rows(a, splits, s));
-  g_launches = shared ? 2 : 1;
+  g_launches = plan.form == Plan::kMemory ? 2 : 1;
   return msa_ok();
 }
 

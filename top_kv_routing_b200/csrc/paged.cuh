@@ -65,6 +65,8 @@ inline size_t memory_bytes(int64_t rows, int splits) {
   return memory_part_bytes(rows, splits) + (size_t)rows * 2 * splits * sizeof(float2);
 }
 cudaError_t launch_memory(const Attend& a, int max_splits, cudaStream_t s);
+// The same kernel's block form: memory and pages of long blocks of new tokens, the whole result.
+cudaError_t launch_blocks(const Attend& a, cudaStream_t s);
 
 // ---- device helpers
 

@@ -10,7 +10,8 @@
 // then the sequence's page rows.  Its keys are cut into tiles of 16.  All tiles of all units,
 // in the order (sequence, layer, key head, row tile, key tile), form one line that is cut
 // into equal pieces, one per warp of the grid (one 8-warp CTA per SM), so that ragged lengths
-// do not leave SMs idle and a single long sequence is spread over all of them.
+// do not leave SMs idle and a single long sequence is spread over all of them.  A unit takes
+// six tiles more on the line than it has (its queries, join and output cost about that).
 //
 // Each warp streams its tiles through its own 3-stage cp.async ring in shared memory (16 K
 // rows and 16 V rows a stage, 16-byte chunks XOR-swizzled by row so ldmatrix is
@@ -40,6 +41,7 @@ constexpr int kRowBytes = kD * 2;
 constexpr int kStageBytes = 2 * kTileKeys * kRowBytes;  // 16 K rows, then 16 V rows
 constexpr int kRingBytes = kRowWarps * kStages * kStageBytes;
 constexpr int kMinTiles = 2;  // tiles per warp below which a unit is not cut further
+constexpr int kUnitTicks = 6; // what a unit costs beyond its tiles (queries in, join, output), in tiles
 
 // The tables of the batch in shared memory.
 struct Tables {
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kPer; ++i) {
       const int b = tid * kPer + i;
       v[i] = sum;
-      if (b < a.B) sum += (int64_t)row_tiles(b) * key_tiles(b);
+      if (b < a.B) sum += (int64_t)row_tiles(b) * (key_tiles(b) + kUnitTicks);
     }
     int64_t inc = sum;
 #pragma unroll
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_layer(c);
   };
   Cursor c;
+  int64_t at = w0;  // the position of cursor c on the line
   {
     int lo = 0, hi = a.B;  // scan[lo] * LH <= w0 < scan[hi] * LH
     while (hi - lo > 1) {
@@ -224,14 +227,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     c.b = lo;
     set_sequence(c);
-    const int64_t rem = w0 - tb.scan[lo] * LH, each = (int64_t)c.RT * c.nt;
+    const int64_t rem = w0 - tb.scan[lo] * LH, unit = c.nt + kUnitTicks, each = c.RT * unit;
     c.lh = (int)(rem / each);
     const int64_t in = rem - c.lh * each;
-    c.rt = (int)(in / c.nt);
-    c.j = (int)(in - (int64_t)c.rt * c.nt);
+    c.rt = (int)(in / unit);
+    c.j = (int)(in - (int64_t)c.rt * unit);
     set_layer(c);
+    if (c.j >= c.nt) {  // behind the unit's last tile
+      at += unit - c.j;
+      next_unit(c);
+    }
   }
   Cursor pc = c;  // the loads run ahead of the arithmetic
+  int64_t pat = at;
 
   const uint32_t my_ring = smem_u32(smem_raw) + warp * (kStages * kStageBytes);
   // page ids of 32 consecutive tiles of a sequence, one per lane
@@ -244,8 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int rows;
     bad &= ~(1u << stage);
     if (!PART && pc.j < pc.mt) {
-      const int64_t at = (((int64_t)tb.grp[pc.b] * a.L + pc.l) * 2 * a.H + pc.h) * a.M_max + pc.j * kTileKeys;
-      kp = a.mem_kv + at * kD;
+      const int64_t row = (((int64_t)tb.grp[pc.b] * a.L + pc.l) * 2 * a.H + pc.h) * a.M_max + pc.j * kTileKeys;
+      kp = a.mem_kv + row * kD;
       vp = kp + (int64_t)a.H * a.M_max * kD;
       rows = pc.M - pc.j * kTileKeys;
     } else {
@@ -266,8 +274,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         rows = 0;
         kp = vp = a.pages;
       } else {
-        const int64_t at = ((((int64_t)pc.l * a.NP + id) * 2 * a.H + pc.h) << a.log2_page) + ((jj * kTileKeys) & page_mask);
-        kp = a.pages + at * kD;
+        const int64_t row =
+            ((((int64_t)pc.l * a.NP + id) * 2 * a.H + pc.h) << a.log2_page) + ((jj * kTileKeys) & page_mask);
+        kp = a.pages + row * kD;
         vp = kp + ((int64_t)a.H << a.log2_page) * kD;
       }
     }
@@ -281,13 +290,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const __nv_bfloat16* src = (u < 8 ? kp : vp) + (ok ? key * kD + chunk * 8 : 0);
       cp_async16(st + row * kRowBytes + ((chunk ^ (row & 7)) << 4), src, ok ? 16u : 0u);
     }
-    if (++pc.j == pc.nt) next_unit(pc);
+    ++pat;
+    if (++pc.j == pc.nt) {
+      pat += kUnitTicks;
+      next_unit(pc);
+    }
   };
 
-  const int n_tiles = (int)min((int64_t)0x7fffffff, w1 - w0);
 #pragma unroll
   for (int p = 0; p < kStages; ++p) {
-    if (p < n_tiles) issue(p);
+    if (pat < w1) issue(p);
     cp_async_commit();
   }
 
@@ -296,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float m[NR], lsum[NR];
   int lim[NR];  // the last page row that this thread's rows see
   bool fresh = true, memory_done = false;
-  int64_t u0 = w0 - c.j;  // the unit's first tile on the line
+  int64_t u0 = at - c.j;  // the unit's first tile on the line
 
   // a row's token within the sequence, and its place among the rows of q and out
   auto row_token = [&](int r) -> int { return c.rt * kTok + r / G; };
@@ -304,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (((int64_t)c.l * a.T + tb.tok0[c.b] + row_token(r)) * Hq + c.h * G + r % G) * kD;
   };
 
-  for (int i = 0; i < n_tiles; ++i) {
+  for (int i = 0; at < w1; ++i) {
     if (fresh) {  // a new unit: its queries (row g in words 0 and 1 of the A fragment, row g + 8)
       fresh = false;
 #pragma unroll
@@ -458,11 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();  // every lane is done with the stage: refill it with tile i + 3
-    if (i + kStages < n_tiles) issue(i + kStages);
+    if (pat < w1) issue(i + kStages);
     cp_async_commit();
 
     const bool unit_end = c.j + 1 == c.nt;
-    if (unit_end || i + 1 == n_tiles) {
+    ++at;
+    if (unit_end || at == w1) {
       // ---- the unit (or this piece of it) is done
       float sum[NR];
 #pragma unroll
@@ -592,8 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (unit_end && i + 1 < n_tiles) {
-        u0 = u1;
+      at += kUnitTicks;  // (past w1 where the piece ends within the unit)
+      if (at < w1) {
+        u0 = at;
         next_unit(c);
         fresh = true;
       }

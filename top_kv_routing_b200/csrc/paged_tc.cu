@@ -1,32 +1,43 @@
-// Shared-memory attention of a paged batch on the tcgen05 tensor cores: the memory part, all
-// new tokens of a group at once.
+// Shared-memory attention of a paged batch on the tcgen05 tensor cores, 256 rows a CTA, in two
+// forms (msa_paged.h defines the result):
+//   memory form  the packed tokens of a group (all of its sequences' new tokens) x the G query
+//                heads of key head h are the MMA's rows, so every tile of the group's memory is
+//                read once per 256 rows whatever the number of sequences.  A unit is (group,
+//                layer, key head, pair of row tiles, key split); its result per row and split,
+//                the unnormalised fp32 output, its maximum and its sum, is joined with the
+//                sequence's own pages by the row kernel (paged_rows.cu).
+//   block form   for long blocks of new tokens: a unit is (sequence, layer, key head, pair of
+//                row tiles of its tokens) over the memory and then the sequence's pages, causal,
+//                and writes the output itself.
 //
 // Follows "MSA端到端可训练记忆模型完整开源，支持亿级Token上下文", section 架构 (softmax over the
 // selected memory joined to the local K/V), and the MSA paper reading notes, section
 // 推理全流程.
 //
-// The packed tokens of a group (all of its sequences' new tokens) x the G query heads of key
-// head h are the MMA's rows, 128 a row tile, so every tile of keys is read once per 256 rows
-// whatever the number of sequences.  A unit is (group, layer, key head, pair of row tiles,
-// key split).  Persistent CTAs (one per SM) of 320 threads walk the units:
-//   warp 9 (one thread)  TMA: the unit's query rows (4D box), then 128-key tiles of K and V in
-//                        the order the MMAs use them, through a ring of 32 KB slots;
+// Persistent CTAs (one per SM) of 384 threads walk the units:
+//   warp 9               TMA: the unit's query rows (4D box), then 128-key tiles of K and V in
+//                        the order the MMAs use them, through a ring of 32 KB slots (memory
+//                        tiles as 64-row boxes, page tiles as one box per page, a lane each);
 //   warp 8               MMA issue for two streams a and b: S = Q K^T (queries from shared
 //                        memory, M = N = 128), O += P V (weights from tensor memory, written
 //                        over their scores; V read MN-major from its rows).  PV_a(j), S_a(j+1),
 //                        PV_b(j), S_b(j+1), ...: while one stream's softmax runs, the tensor
 //                        cores work for the other;
-//   warps 0..3, 4..7     the softmax of stream a and of stream b: a thread per row.  A running
-//                        maximum that is raised (and O rescaled in tensor memory) only when a
-//                        score exceeds it by more than 2^8; weights exp2(s - m) rounded to
-//                        bf16 (the MMA's operand type; the row sum takes them unrounded).
+//   warps 0..3, 4..7     the softmax of stream a and of stream b: a thread per row, with the
+//                        registers that warps 8..11 give up.  A running maximum that is raised
+//                        (and O rescaled in tensor memory) only when a score exceeds it by more
+//                        than 2^8; weights exp2(s - m) rounded to bf16 (the MMA's operand type;
+//                        the row sum takes them unrounded).
 // Streams a and b are the two row tiles of the pair over the same keys.  A group of at most
 // one row tile gives both streams the same rows and each half of the unit's keys instead.
-// Output: per row and key split the unnormalised fp32 output, its maximum and its sum, which
-// the row kernel (paged_rows.cu) joins with the sequence's own pages.
+//
+// The exponentials bound the softmax: 2 x 16,384 per tile pair at 16 a clock take as long as
+// its MMAs (2,048 clocks), so kPolyOf8 of every 8 are computed on the FMA pipe instead: round x
+// to an integer n by the 1.5 x 2^23 addition, a minimax polynomial of degree 4 for 2^(x - n) on
+// [-1/2, 1/2] (Remez exchange, relative error 2.6e-6), n added to the exponent bits.
 //
 // S_x(j + 1) is issued after PV_x(j), so its completion also says that O_x is stable: the
-// softmax rescales it without another wait.  Key rows past the memory's length are zeroed in
+// softmax rescales it without another wait.  Key rows past the last valid one are zeroed in
 // shared memory before the PV that reads them (they may hold anything).  Every wait is
 // bounded (2 s); a timeout sets MSA_DEVERR_TIMEOUT and the CTA drains and frees its TMEM.
 #include <cuda.h>
@@ -47,22 +58,33 @@ constexpr int kHalf = 64;                 // dims of a 128-byte swizzled row
 constexpr int kHalfBytes = kTile * 128;   // 16 KB: 128 rows x 64 dims
 constexpr int kSlotBytes = 2 * kHalfBytes;  // one K or V tile, or one query tile
 constexpr int kSlots = 4;
-constexpr int kWarpsTc = 10;
+constexpr int kWarpsTc = 12;              // 0..7 softmax, 8 MMA, 9 TMA, 10 and 11 none
 constexpr int kThreadsTc = kWarpsTc * 32;
+// registers: 168 a thread at launch; 128 x 80 + 256 x 208 <= 384 x 168
+constexpr int kRegsIssue = 80, kRegsSoftmax = 208;
+static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreadsTc * 168, "register split");
+constexpr int kPolyOf8 = 2;               // of every 8 exponentials, those on the FMA pipe
 constexpr int kMmaWarp = 8, kTmaWarp = 9;
 constexpr uint32_t kTmemCols = 512;       // S_a | S_b | O_a | O_b
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kHeadroom = 8.0f;         // log2 growth of a row's maximum tolerated before rescaling
 
+constexpr int kBadRing = 8;               // tiles whose page masks are kept (more than are in flight)
+
+// The batch in shared memory: an entry is a group (memory form) or a sequence (block form).
 struct TablesTc {
-  int scan[kMaxSeqs + 1];  // row-tile pairs of the groups before g
+  int scan[kMaxSeqs + 1];  // row-tile pairs of the entries before
   int lo[kMaxSeqs];        // first token
   int n[kMaxSeqs];         // tokens
+  int len[kMaxSeqs];       // block form: page rows, as given
+  int grp[kMaxSeqs];       // block form: group, or -1
   int warp_sum[kWarpsTc];
-  int most;                // most key tiles of any (group, layer)
+  int most;                // memory form: most key tiles of any (group, layer)
   int splits;
   uint32_t tmem;
   int abort;
+  int poison[2];           // block form, by stream: units + 1 of its last one with values cleared
+  uint32_t bad[kBadRing];  // block form: per tile, its 16-row pieces without a usable page
 };
 
 constexpr int kOffQ = 0;
@@ -102,27 +124,101 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ void st_global_v8(float* p, const float (&x)[8]) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&x)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+               "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                : "memory");
+}
+
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
+};
+
+// Packed pairs of fp32 (two registers).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// the largest of three, NaN if any is
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 2^x for two finite x <= 126 on the FMA pipe (below 2^-125: 2^-125): n = round(x), a minimax
+// polynomial for 2^(x - n) on [-1/2, 1/2], n added to the exponent.
+__device__ __forceinline__ void ex2_poly(f32x2 x2, float& y0, float& y1) {
+  float x0, x1;
+  unpack2(x2, x0, x1);
+  x2 = pack2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
+  const f32x2 t = add2(x2, pack2(12582912.f, 12582912.f));
+  const f32x2 n = add2(t, pack2(-12582912.f, -12582912.f));
+  const f32x2 f = fma2(n, pack2(-1.f, -1.f), x2);
+  f32x2 p = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
+                 pack2(0.05591785907745361f, 0.05591785907745361f));
+  p = fma2(p, f, pack2(0.240247443318367f, 0.240247443318367f));
+  p = fma2(p, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+  p = fma2(p, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  float p0, p1, t0, t1;
+  unpack2(p, p0, p1);
+  unpack2(t, t0, t1);
+  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 
 // One unit as every role sees it.
 struct Unit {
-  int l, h;
+  int e, l, h;               // entry, layer, key head
   int tok[2], n_tok[2];      // each stream's tokens
   int t0[2], t1[2];          // each stream's key tiles [t0, t1)
-  int M;                     // memory rows
+  int M, mt;                 // memory rows and tiles (the page tiles follow)
+  int n_loc;                 // page rows that some row sees
+  int lim0;                  // page rows that the first token sees (token i: i more, up to len)
+  int len;                   // page rows (clamped)
   bool shared;               // the streams read the same key tiles
   int64_t kv_row;            // row of key 0 in the memory tensor; values H * M_max further
   int slot[2];               // partial slot
 };
 
-template <int G>
+// Adds the values that are not finite of the page tiles that were cleared of them (those a row
+// of the pair does not see in full), as far as this row sees them, to its 32 dims from d0.
+__device__ __forceinline__ void add_not_finite(const Attend& a, const Unit& x, int seen, int d0, uint32_t (&o)[32]) {
+  const int page = 1 << a.log2_page;
+#pragma unroll 1
+  for (int k = max(0, x.lim0) / kTile * kTile; k < seen; ++k) {
+    const int id = a.page_table[(int64_t)x.e * a.max_pages + (k >> a.log2_page)];
+    if (id < 0 || id >= a.NP) continue;
+    const int64_t row = ((((((int64_t)x.l * a.NP + id) * 2 + 1) * a.H + x.h)) << a.log2_page) + (k & (page - 1));
+    for (int e = 0; e < 32; ++e) {
+      const float v = __bfloat162float(a.pages[row * kD + d0 + e]);
+      if (!(fabsf(v) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
+    }
+  }
+}
+
+template <int G, bool BLOCK>
 __global__ void __launch_bounds__(kThreadsTc, 1)
-    memory_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                  const __grid_constant__ Attend a, int max_splits) {
+    tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                const __grid_constant__ CUtensorMap tm_pages, const __grid_constant__ Attend a, int max_splits) {
   constexpr int kTok = kRows / G;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -155,6 +251,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
     mbar_init(smem_u32(drain), 1);
     tb.abort = 0;
+    tb.poison[0] = tb.poison[1] = 0;
     tb.most = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
@@ -166,7 +263,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   wait_for_earlier_kernels();
   let_next_kernel_start();
 
-  // ---- tables: tokens and row-tile pairs of every group
+  // ---- tables: tokens and row-tile pairs of every entry
+  const int n_entries = BLOCK ? a.B : a.NG;
+  const int64_t cap = (int64_t)a.max_pages << a.log2_page;
   const bool groups_ok = group_offsets_usable(a, tid, kThreadsTc);  // (a barrier for all threads)
   if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
   {
@@ -174,13 +273,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     int v[kPer], sum = 0, most = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int g = tid * kPer + i;
+      const int e = tid * kPer + i;
       v[i] = sum;
-      if (g < a.NG) {
-        int lo, n;
-        if (!groups_ok || !group_tokens(a, g, lo, n)) n = 0;
-        tb.lo[g] = lo;
-        tb.n[g] = n;
+      if (e < n_entries) {
+        int lo = 0, n = 0;
+        if (BLOCK) {
+          if (!sequence_tokens(a.q_offsets, e, a.T, lo, n) && blockIdx.x == 0)
+            msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+          const int len = a.seq_len[e];
+          if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
+          tb.len[e] = len;
+          tb.grp[e] = -1;
+        } else if (!groups_ok || !group_tokens(a, e, lo, n)) {
+          n = 0;
+        }
+        tb.lo[e] = lo;
+        tb.n[e] = n;
         sum += (n + 2 * kTok - 1) / (2 * kTok);
       }
     }
@@ -205,27 +313,32 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     for (int w = 0; w < warp; ++w) base += tb.warp_sum[w];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int g = tid * kPer + i;
-      if (g < a.NG) tb.scan[g] = base + v[i];
+      const int e = tid * kPer + i;
+      if (e < n_entries) tb.scan[e] = base + v[i];
     }
-    if (tid == kThreadsTc - 1) tb.scan[a.NG] = base + sum;
+    if (tid == kThreadsTc - 1) tb.scan[n_entries] = base + sum;
   }
+  if (BLOCK && groups_ok)
+    for (int g = warp; g < a.NG; g += kWarpsTc)
+      for (int b = a.group_offsets[g] + lane; b < a.group_offsets[g + 1]; b += 32) tb.grp[b] = g;
   __syncthreads();
-  const int pairs = tb.scan[a.NG];
+  const int pairs = tb.scan[n_entries];
   if (tid == 0) {
-    // the split that finishes first, a unit costing its tiles and about two more
-    const int64_t units = (int64_t)pairs * LH;
     int best = 1;
-    int64_t cost = INT64_MAX;
-    for (int s = 1; s <= max_splits && s <= max(1, tb.most); ++s) {
-      const int64_t c = (units * s + gridDim.x - 1) / gridDim.x * ((tb.most + s - 1) / s + 2);
-      if (c < cost) {
-        cost = c;
-        best = s;
+    if (!BLOCK) {
+      // the split that finishes first, a unit costing its tiles and about two more
+      const int64_t units = (int64_t)pairs * LH;
+      int64_t cost = INT64_MAX;
+      for (int s = 1; s <= max_splits && s <= max(1, tb.most); ++s) {
+        const int64_t c = (units * s + gridDim.x - 1) / gridDim.x * ((tb.most + s - 1) / s + 2);
+        if (c < cost) {
+          cost = c;
+          best = s;
+        }
       }
+      if (blockIdx.x == 0) *reinterpret_cast<int*>(a.ws + kWsSplits) = best;
     }
     tb.splits = best;
-    if (blockIdx.x == 0) *reinterpret_cast<int*>(a.ws + kWsSplits) = best;
   }
   __syncthreads();
   const int splits = tb.splits;
@@ -234,123 +347,194 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 
   auto unit_at = [&](int64_t u) -> Unit {
     Unit x;
-    const int pair = (int)(u % pairs);
-    const int64_t rest = u / pairs;
-    const int s = (int)(rest % splits), lh = (int)(rest / splits);
+    // memory form: pairs run fastest (CTAs at work together read the same keys); block form:
+    // (layer, key head) runs fastest, and the sequences' last pairs, which see the most, first
+    const int64_t rest = BLOCK ? u / LH : u / pairs;
+    const int pair = BLOCK ? pairs - 1 - (int)rest : (int)(u - rest * pairs);
+    const int s = BLOCK ? 0 : (int)(rest % splits);
+    const int lh = BLOCK ? (int)(u - rest * LH) : (int)(rest / splits);
     x.l = lh / a.H;
     x.h = lh - x.l * a.H;
-    int lo = 0, hi = a.NG;  // scan[lo] <= pair < scan[hi]
+    int lo = 0, hi = n_entries;  // scan[lo] <= pair < scan[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (tb.scan[mid] <= pair) lo = mid; else hi = mid;
     }
-    const int64_t gl = (int64_t)lo * a.L + x.l;
-    x.M = max(0, min(a.M_max, __ldg(a.mem_len + gl)));
+    x.e = lo;
+    const int g = BLOCK ? tb.grp[lo] : lo;
+    const int64_t gl = (int64_t)g * a.L + x.l;
+    x.M = g < 0 ? 0 : max(0, min(a.M_max, __ldg(a.mem_len + gl)));
     x.kv_row = (gl * 2 * a.H + x.h) * a.M_max;
-    const int nt = (x.M + kTile - 1) / kTile;
+    x.mt = (x.M + kTile - 1) / kTile;
     const int at = (pair - tb.scan[lo]) * 2 * kTok, n = tb.n[lo];
-    x.shared = n > kTok;
     x.tok[0] = tb.lo[lo] + at;
     x.n_tok[0] = min(kTok, n - at);
-    if (x.shared) {
-      const int per = (nt + splits - 1) / splits;
+    x.n_loc = x.lim0 = x.len = 0;
+    x.slot[0] = x.slot[1] = s;
+    x.shared = BLOCK || n > kTok;
+    if (BLOCK) {
       x.tok[1] = x.tok[0] + kTok;
       x.n_tok[1] = max(0, min(kTok, n - at - kTok));
-      x.t0[0] = x.t0[1] = min(nt, s * per);
-      x.t1[0] = min(nt, s * per + per);
+      x.len = (int)min((int64_t)max(tb.len[lo], 0), cap);
+      x.lim0 = max(tb.len[lo], 0) - n + at + 1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int seen = max(0, min(x.lim0 + x.n_tok[0] - 1 + i * x.n_tok[1], x.len));
+        x.t0[i] = 0;
+        x.t1[i] = x.n_tok[i] > 0 ? x.mt + (seen + kTile - 1) / kTile : 0;
+        x.n_loc = max(x.n_loc, seen);
+      }
+    } else if (x.shared) {
+      const int per = (x.mt + splits - 1) / splits;
+      x.tok[1] = x.tok[0] + kTok;
+      x.n_tok[1] = max(0, min(kTok, n - at - kTok));
+      x.t0[0] = x.t0[1] = min(x.mt, s * per);
+      x.t1[0] = min(x.mt, s * per + per);
       x.t1[1] = x.n_tok[1] > 0 ? x.t1[0] : x.t0[1];  // (no rows: no tiles)
-      x.slot[0] = x.slot[1] = s;
     } else {
-      const int per = (nt + 2 * splits - 1) / (2 * splits);
+      const int per = (x.mt + 2 * splits - 1) / (2 * splits);
       x.tok[1] = x.tok[0];
       x.n_tok[1] = x.n_tok[0];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         x.slot[i] = 2 * s + i;
-        x.t0[i] = min(nt, x.slot[i] * per);
-        x.t1[i] = min(nt, x.slot[i] * per + per);
+        x.t0[i] = min(x.mt, x.slot[i] * per);
+        x.t1[i] = min(x.mt, x.slot[i] * per + per);
       }
     }
     return x;
   };
+  // valid keys of a tile (for the pair: a single row may see fewer)
+  auto valid_keys = [&](const Unit& x, int tile) -> int {
+    return !BLOCK || tile < x.mt ? min(kTile, x.M - tile * kTile) : min(kTile, x.n_loc - (tile - x.mt) * kTile);
+  };
 
+  // (in each role's own branch: the compiler allocates what follows by it)
   if (warp == kTmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    // ---- loads: the warp walks together (a lane per page box), lane 0 arms and waits
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
-      bool ok = true;
-      uint32_t it = 0;                 // ring position
-      int armed[kSlots], q_armed[2] = {-1, -1};
-#pragma unroll
-      for (int s = 0; s < kSlots; ++s) armed[s] = -1;
-      uint32_t qn[2] = {0, 0};         // query tiles loaded per stream
-      auto load = [&](const Unit& x, int tile, bool is_v) {
-        if (!ok) return;
-        const int slot = it % kSlots;
-        const uint32_t ph = (it / kSlots) & 1u;
-        if (!mbar_wait(smem_u32(&empty[slot]), ph ^ 1u, abort_flag)) {
-          ok = false;
-          return;
+      if (BLOCK) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_pages)) : "memory");
+    }
+    bool ok = true;
+    uint32_t it = 0;                // ring position
+    uint32_t tiles = 0;             // key tiles of the block form so far
+    uint32_t qn[2] = {0, 0};        // query tiles loaded per stream
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
+      return ok;
+    };
+    // page ids of 512 consecutive rows of a sequence, a lane per 16 rows
+    int ids_e = -1, ids_win = -1, ids = 0;
+    const int log2_box = min(6, a.log2_page);  // rows of a page box: the page, at most 64
+    auto load = [&](const Unit& x, int tile, bool is_v) {
+      if (!ok) return;
+      const int slot = it % kSlots;
+      if (!wait(&empty[slot], ((it / kSlots) & 1u) ^ 1u)) return;
+      ++it;
+      const uint32_t bar = smem_u32(&full[slot]);
+      const uint32_t dst = sbase + kOffRing + slot * kSlotBytes;
+      const int valid = valid_keys(x, tile);
+      if (!BLOCK || tile < x.mt) {
+        if (lane == 0) {
+          const int boxes = valid > kBox ? 2 : 1;
+          const int row = (int)(x.kv_row + (is_v ? (int64_t)a.H * a.M_max : 0) + tile * kTile);
+          if (BLOCK && !is_v) tb.bad[tiles % kBadRing] = 0u;
+          mbar_arrive_expect_tx(bar, boxes * 2 * kBox * 128);
+          for (int b = 0; b < boxes; ++b) {
+            tma_load_rows(dst + b * kBox * 128, &tm_kv, bar, 0, row + b * kBox);
+            tma_load_rows(dst + kHalfBytes + b * kBox * 128, &tm_kv, bar, kHalf, row + b * kBox);
+          }
         }
-        const int key0 = tile * kTile;
-        const int boxes = x.M - key0 > kBox ? 2 : 1;
-        const uint32_t bar = smem_u32(&full[slot]);
-        const uint32_t dst = sbase + kOffRing + slot * kSlotBytes;
-        const int row = (int)(x.kv_row + (is_v ? (int64_t)a.H * a.M_max : 0) + key0);
-        mbar_arrive_expect_tx(bar, boxes * 2 * kBox * 128);
-        for (int b = 0; b < boxes; ++b) {
-          tma_load_rows(dst + b * kBox * 128, &tm_kv, bar, 0, row + b * kBox);
-          tma_load_rows(dst + kHalfBytes + b * kBox * 128, &tm_kv, bar, kHalf, row + b * kBox);
+      } else {
+        const int key0 = (tile - x.mt) * kTile;
+        if (ids_e != x.e || ids_win != (key0 >> 9)) {
+          ids_e = x.e;
+          ids_win = key0 >> 9;
+          const int row = (ids_win << 9) + lane * 16;
+          ids = row < x.len ? __ldg(a.page_table + (int64_t)x.e * a.max_pages + (row >> a.log2_page)) : 0;
         }
-        armed[slot] = (int)ph;
-        ++it;
-      };
-      auto load_q = [&](const Unit& x, int st) {
-        if (!ok) return;
-        if (!mbar_wait(smem_u32(&q_empty[st]), (qn[st] & 1u) ^ 1u, abort_flag)) {
-          ok = false;
-          return;
+        const int boxes = (valid + (1 << log2_box) - 1) >> log2_box;
+        // lane b < boxes: rows [b << log2_box, ...) of the tile
+        const int id = __shfl_sync(0xffffffffu, ids, ((key0 & 511) >> 4) + ((lane << log2_box) >> 4 & 7));
+        const bool use = lane < boxes;
+        const bool bad = use && (id < 0 || id >= a.NP);
+        const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) {
+          if (!is_v) {
+            uint32_t mask = 0u;
+            for (int b = 0; b < boxes; ++b)
+              if ((bads >> b) & 1u) mask |= ((1u << (1 << (log2_box - 4))) - 1u) << (b << (log2_box - 4));
+            tb.bad[tiles % kBadRing] = mask;
+            if (bads) msa::set_err(a.dev_err, MSA_DEVERR_BAD_PAGE);
+          }
+          mbar_arrive_expect_tx(bar, (uint32_t)boxes * 2u * (128u << log2_box));
         }
+        __syncwarp();
+        if (use) {
+          // (a bad page's box starts past the tensor's end and reads as zeros)
+          const int64_t first = ((((int64_t)x.l * a.NP + id) * 2 + (is_v ? 1 : 0)) * a.H + x.h) << a.log2_page;
+          const int64_t past = ((int64_t)a.L * a.NP * 2 * a.H) << a.log2_page;
+          const int row = (int)(bad ? past : first + ((key0 + (lane << log2_box)) & ((1 << a.log2_page) - 1)));
+          const uint32_t to = dst + (uint32_t)(lane << log2_box) * 128u;
+          tma_load_rows(to, &tm_pages, bar, 0, row);
+          tma_load_rows(to + kHalfBytes, &tm_pages, bar, kHalf, row);
+        }
+      }
+      if (BLOCK && !is_v) ++tiles;
+      __syncwarp();
+    };
+    auto load_q = [&](const Unit& x, int st) {
+      if (!ok) return;
+      if (!wait(&q_empty[st], (qn[st] & 1u) ^ 1u)) return;
+      ++qn[st];
+      if (lane == 0) {
         const uint32_t bar = smem_u32(&q_full[st]);
         const uint32_t dst = sbase + kOffQ + st * kSlotBytes;
         mbar_arrive_expect_tx(bar, kSlotBytes);
         tma_load_4d(dst, &tm_q, bar, 0, x.h * G, x.tok[st], x.l);
         tma_load_4d(dst + kHalfBytes, &tm_q, bar, kHalf, x.h * G, x.tok[st], x.l);
-        q_armed[st] = (int)(qn[st] & 1u);
-        ++qn[st];
-      };
-      for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-        const Unit x = unit_at(u);
-        const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
-        if (n0 > 0) {
-          load_q(x, 0);
-          load(x, x.t0[0], false);
-        }
-        if (n1 > 0) {
-          load_q(x, 1);
-          if (!x.shared) load(x, x.t0[1], false);
-        }
-        for (int j = 0; j < max(n0, n1) && ok; ++j) {
-          if (j < n0) {
-            load(x, x.t0[0] + j, true);
-            if (j + 1 < n0) load(x, x.t0[0] + j + 1, false);
-          }
-          if (!x.shared && j < n1) {
-            load(x, x.t0[1] + j, true);
-            if (j + 1 < n1) load(x, x.t0[1] + j + 1, false);
-          }
-        }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
-        for (int s = 0; s < kSlots; ++s)
-          if (armed[s] >= 0) mbar_drain(smem_u32(&full[s]), (uint32_t)armed[s]);
-        for (int st = 0; st < 2; ++st)
-          if (q_armed[st] >= 0) mbar_drain(smem_u32(&q_full[st]), (uint32_t)q_armed[st]);
+      __syncwarp();
+    };
+    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+      const Unit x = unit_at(u);
+      const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
+      // tile j of stream b is loaded for it alone
+      auto own_b = [&](int j) { return j < n1 && (!x.shared || j >= n0); };
+      if (n0 > 0) {
+        load_q(x, 0);
+        load(x, x.t0[0], false);
+      }
+      if (n1 > 0) {
+        load_q(x, 1);
+        if (own_b(0)) load(x, x.t0[1], false);
+      }
+      for (int j = 0; j < max(n0, n1) && ok; ++j) {
+        if (j < n0) {
+          load(x, x.t0[0] + j, true);
+          if (j + 1 < n0) load(x, x.t0[0] + j + 1, false);
+        }
+        if (own_b(j)) load(x, x.t0[1] + j, true);
+        if (own_b(j + 1)) load(x, x.t0[1] + j + 1, false);
       }
     }
+    if (!ok) {
+      // wait (bounded) for the copies in flight: the last kSlots loads and the last query tiles
+      if (lane == 0) {
+        *abort_flag = 1;
+        msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
+        for (uint32_t p = it > kSlots ? it - kSlots : 0; p < it; ++p)
+          mbar_drain(smem_u32(&full[p % kSlots]), (p / kSlots) & 1u);
+        for (int st = 0; st < 2; ++st)
+          if (qn[st] > 0) mbar_drain(smem_u32(&q_full[st]), (qn[st] - 1) & 1u);
+      }
+      __syncwarp();
+    }
   } else if (warp == kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // the warp waits together, one elected lane issues
     const bool leader = elect_one();
     constexpr uint32_t idesc_s = idesc_make(kRows, kTile, false);
@@ -364,6 +548,36 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
       if (ok) tc_fence_after();
       return ok;
+    };
+    // Values that are not finite must not reach the rows that do not see them (0 x inf is NaN):
+    // they are cleared, and the unit is marked for each stream before its last PV (a stream is
+    // then still in this unit); its rows add what they see of them at the end.
+    bool cleared = false;
+    auto clear_not_finite = [&](uint32_t vt, int rows) {
+      bool any = false;
+      for (int i = lane; i < rows * 16; i += 32) {
+        const uint32_t at = vt + (uint32_t)((i & 8 ? kHalfBytes : 0) + (i >> 4) * 128 + (i & 7) * 16);
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at)
+                     : "memory");
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, bad = true;
+          if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0x0000FFFFu, bad = true;
+        }
+        if (bad)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                       : "memory");
+        any |= bad;
+      }
+      if (__any_sync(0xffffffffu, any)) {
+        cleared = true;
+        fence_async_smem();
+        __syncwarp();
+      }
     };
     // scores of stream st over its key tile in ring position `pos`; `release`: the tile's last use
     auto score = [&](int st, uint32_t pos, bool release, bool last) {
@@ -386,14 +600,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       issued = true;
       __syncwarp();
     };
-    auto weigh = [&](int st, uint32_t pos, int valid, bool first, bool release, bool last) {
+    auto weigh = [&](int st, uint32_t pos, int valid, bool first, bool release, bool last, bool check, int unit) {
       if (!ok) return;
       if (!wait(&p_ready[st], pn[st] & 1u)) return;
       ++pn[st];
       if (!wait(&full[pos % kSlots], (pos / kSlots) & 1u)) return;
       const uint32_t vt = sbase + kOffRing + (pos % kSlots) * kSlotBytes;
       const int n_ks = min(kTile, valid + 15) / 16;  // 16-key steps
-      if (valid < n_ks * 16) {  // rows past the memory's end may hold anything
+      if (valid < n_ks * 16) {  // rows past the last valid one may hold anything
         for (int i = lane; i < (n_ks * 16 - valid) * 16; i += 32) {
           const int row = valid + (i >> 4), c16 = i & 15;
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (uint32_t)((c16 >> 3) * kHalfBytes + row * 128 +
@@ -402,6 +616,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                        : "memory");
         }
         fence_async_smem();
+        __syncwarp();
+      }
+      if (BLOCK && check) clear_not_finite(vt, n_ks * 16);
+      if (BLOCK && last && cleared) {
+        if (lane == 0) tb.poison[st] = unit + 1;
+        __threadfence_block();
         __syncwarp();
       }
       if (leader) {
@@ -415,38 +635,43 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       __syncwarp();
     };
-    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+    int64_t u = blockIdx.x;
+    for (int un = 0; u < n_units && ok; u += gridDim.x, ++un) {
       const Unit x = unit_at(u);
+      cleared = false;
       const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
-      const bool both = x.shared && n1 > 0;  // stream b reads stream a's tiles
-      auto valid = [&](int tile) { return min(kTile, x.M - tile * kTile); };
+      auto with_a = [&](int j) { return x.shared && j < n0; };  // stream b reads stream a's tile j
+      auto with_b = [&](int j) { return x.shared && j < n1; };
+      // a page tile that some rows of the pair do not see in full
+      auto edge = [&](int tile) { return BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0; };
       auto q_wait = [&](int st) {
         if (ok && wait(&q_full[st], qn[st] & 1u)) ++qn[st];
       };
       if (n0 > 0) {
         q_wait(0);
         kpos = it++;
-        score(0, kpos, !both, n0 == 1);
+        score(0, kpos, !with_b(0), n0 == 1);
       }
       if (n1 > 0) {
         q_wait(1);
-        const uint32_t pos = x.shared ? kpos : it++;
+        const uint32_t pos = with_a(0) ? kpos : it++;
         score(1, pos, true, n1 == 1);
       }
       for (int j = 0; j < max(n0, n1) && ok; ++j) {
         if (j < n0) {
           vpos = it++;
-          weigh(0, vpos, valid(x.t0[0] + j), j == 0, !both, j + 1 == n0);
+          weigh(0, vpos, valid_keys(x, x.t0[0] + j), j == 0, !with_b(j), j + 1 == n0, edge(x.t0[0] + j), un);
           if (j + 1 < n0) {
             kpos = it++;
-            score(0, kpos, !both, j + 2 == n0);
+            score(0, kpos, !with_b(j + 1), j + 2 == n0);
           }
         }
         if (j < n1) {
-          const uint32_t pv = x.shared ? vpos : it++;
-          weigh(1, pv, valid(x.t0[1] + j), j == 0, true, j + 1 == n1);
+          const bool alone = !with_a(j);
+          const uint32_t pv = alone ? it++ : vpos;
+          weigh(1, pv, valid_keys(x, x.t0[1] + j), j == 0, true, j + 1 == n1, alone && edge(x.t0[1] + j), un);
           if (j + 1 < n1) {
-            const uint32_t pk = x.shared ? kpos : it++;
+            const uint32_t pk = with_a(j + 1) ? kpos : it++;
             score(1, pk, true, j + 2 == n1);
           }
         }
@@ -463,7 +688,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         mbar_drain(smem_u32(drain), 0u);
       }
     }
-  } else {
+  } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ---- softmax: stream st, thread = row (TMEM lane)
     const int st = warp >> 2, r = tid & (kRows - 1);
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
@@ -472,14 +698,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     float* part = reinterpret_cast<float*>(a.ws + kWsMemory);
     const int64_t all_rows = (int64_t)a.L * a.T * Hq;
     float2* stat = reinterpret_cast<float2*>(a.ws + kWsMemory + memory_part_bytes(all_rows, max_splits));
+    const f32x2 scale2 = pack2(a.qscale, a.qscale);
     uint32_t sn = 0, on = 0;  // score tiles and units so far
+    uint32_t tiles = 0;       // key tiles of the pairs before (block form)
     bool ok = true;
-    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+    int64_t u = blockIdx.x;
+    for (int un = 0; u < n_units && ok; u += gridDim.x, ++un) {
       const Unit x = unit_at(u);
       const int t0 = x.t0[st], n = x.t1[st] - t0;
-      const bool mine = r / G < x.n_tok[st];
-      const int64_t row = x.slot[st] * all_rows + ((int64_t)x.l * a.T + x.tok[st] + r / G) * Hq + x.h * G + r % G;
-      float m = -INFINITY, sum = 0.f;
+      const int tk = r / G;                     // this row's token in its row tile
+      const bool mine = tk < x.n_tok[st];
+      const int64_t row = x.slot[st] * all_rows + ((int64_t)x.l * a.T + x.tok[st] + tk) * Hq + x.h * G + r % G;
+      // page rows that this row sees
+      const int seen = BLOCK ? max(0, min(x.lim0 + st * kTok + tk, x.len)) : 0;
+      float m = -INFINITY;
+      float sum = 0.f;
       for (int j = 0; j < n; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[st]), sn & 1u, abort_flag))) {
           ok = false;
@@ -491,24 +724,34 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
         tmem_wait_ld();
-        const int valid = x.M - (t0 + j) * kTile;
-        if (valid < kTile) {
+        const bool page = BLOCK && t0 + j >= x.mt;
+        const int valid = page ? seen - (t0 + j - x.mt) * kTile : x.M - (t0 + j) * kTile;
+        const uint32_t bad = BLOCK ? *const_cast<volatile uint32_t*>(&tb.bad[(tiles + j) % kBadRing]) : 0u;
+        bool plain = valid >= kTile && bad == 0u;
+        if (!__all_sync(0xffffffffu, plain)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= valid) sv[c][e] = 0xFF800000u;
+              if (32 * c + e >= valid || (BLOCK && ((bad >> (2 * c + (e >> 4))) & 1u))) sv[c][e] = 0xFF800000u;
+          plain = false;
         }
-        float mx = -INFINITY;
+        float mx[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = max3(__uint_as_float(sv[c][0]), __uint_as_float(sv[c][1]), __uint_as_float(sv[c][2]));
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(sv[c][e]));
-        mx *= a.qscale;  // (qscale > 0)
-        const bool need = mx > m + kHeadroom;
+          for (int e = 3; e < 31; e += 2)
+            mx[c] = max3(mx[c], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+          mx[c] = max3(mx[c], __uint_as_float(sv[c][31]), __uint_as_float(sv[c][31]));
+        }
+        const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.qscale;  // (qscale > 0; NaN kept)
+        // the polynomial takes finite arguments only
+        plain = plain && top > -INFINITY && top < INFINITY;
+        const bool need = top > m + kHeadroom;
         if (__any_sync(0xffffffffu, need)) {
-          const float alpha = need ? ex2_ftz(m - mx) : 1.f;  // 0 while m is still -inf
-          if (need) m = mx;
+          const float alpha = need ? ex2_ftz(m - top) : 1.f;  // 0 while m is still -inf
+          if (need) m = top;
           if (j > 0) {  // (PV(j - 1) is done: its commit came before this tile's scores)
             sum *= alpha;
 #pragma unroll 1
@@ -523,28 +766,42 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
         }
         const float base = m == -INFINITY ? 0.f : m;
-        float add[4] = {0.f, 0.f, 0.f, 0.f};
+        const f32x2 base2 = pack2(-base, -base);
+        f32x2 add[2] = {0ull, 0ull};
+        auto weights = [&](auto mixed) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pw[32];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pw[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t s0 = sv[2 * c + (e >> 4)][2 * (e & 15)], s1 = sv[2 * c + (e >> 4)][2 * (e & 15) + 1];
-            const float p0 = ex2_ftz(fmaf(__uint_as_float(s0), a.qscale, -base));
-            const float p1 = ex2_ftz(fmaf(__uint_as_float(s1), a.qscale, -base));
-            add[2 * (e & 1)] += p0;
-            add[2 * (e & 1) + 1] += p1;
-            pw[e] = msa::float2_to_bf16x2(p0, p1);
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t s0 = sv[2 * c + (e >> 4)][2 * (e & 15)], s1 = sv[2 * c + (e >> 4)][2 * (e & 15) + 1];
+              const f32x2 v = fma2(pack2(__uint_as_float(s0), __uint_as_float(s1)), scale2, base2);
+              float p0, p1;
+              if (decltype(mixed)::value && (e & 3) < kPolyOf8 / 2) {
+                ex2_poly(v, p0, p1);
+              } else {
+                unpack2(v, p0, p1);
+                p0 = ex2_ftz(p0);
+                p1 = ex2_ftz(p1);
+              }
+              add[e & 1] = add2(add[e & 1], pack2(p0, p1));
+              pw[e] = msa::float2_to_bf16x2(p0, p1);
+            }
+            tmem_st32(s_col + 32 * c, pw);
           }
-          tmem_st32(s_col + 32 * c, pw);
-        }
-        sum += (add[0] + add[1]) + (add[2] + add[3]);
+        };
+        if (__all_sync(0xffffffffu, plain)) weights(Yes{}); else weights(No{});
+        float s0, s1;
+        unpack2(add2(add[0], add[1]), s0, s1);
+        sum += s0 + s1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&p_ready[st]));
       }
+      if (BLOCK) tiles += max(x.t1[0], x.t1[1]);
       if (!ok) break;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no key seen: output 0; a NaN sum is kept)
       if (n > 0) {
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[st]), on & 1u, abort_flag))) {
           ok = false;
@@ -552,29 +809,44 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         }
         ++on;
         tc_fence_after();
+      }
+      const bool poisoned = BLOCK && *const_cast<volatile int*>(&tb.poison[st]) == un + 1;
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
           tmem_ld32(o_col + 32 * c, o);
           tmem_wait_ld();
-          if (mine) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float w[8];
-#pragma unroll
-              for (int v = 0; v < 8; ++v) w[v] = __uint_as_float(o[8 * e + v]);
-              st_global_v8(part + row * kD + 32 * c + 8 * e, w);
-            }
-          }
         }
-        tc_fence_before();  // (O is read: the next unit's first PV may overwrite it)
+        if (BLOCK && !(n > 0)) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (mine && poisoned) add_not_finite(a, x, seen, 32 * c, o);
+        if (mine && BLOCK) {
+          __nv_bfloat16* dst = a.out + row * kD + 32 * c;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[8];
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              w[v] = msa::float2_to_bf16x2(__uint_as_float(o[16 * e + 2 * v]) * inv, __uint_as_float(o[16 * e + 2 * v + 1]) * inv);
+            st_global_v8(dst + 16 * e, w);
+          }
+        } else if (mine && n > 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st_global_v8(part + row * kD + 32 * c + 8 * e, *reinterpret_cast<uint32_t(*)[8]>(&o[8 * e]));
+        }
       }
-      if (mine) stat[row] = make_float2(m, sum);  // (no tiles: -inf and 0)
+      tc_fence_before();  // (O is read: the next unit's first PV may overwrite it)
+      if (!BLOCK && mine) stat[row] = make_float2(m, sum);  // (no tiles: -inf and 0)
     }
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
     }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
   }
 
   tc_fence_before();
@@ -601,14 +873,14 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 rows of 128 elements, box [64 rows][64 elements], 128-byte swizzle; rows past the end
+// bf16 rows of 128 elements, box [box_rows][64 elements], 128-byte swizzle; rows past the end
 // read as zero
-bool make_kv_map(CUtensorMap* m, const void* base, uint64_t rows) {
+bool make_kv_map(CUtensorMap* m, const void* base, uint64_t rows, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kHalf, (cuuint32_t)kBox};
+  const cuuint32_t box[2] = {(cuuint32_t)kHalf, (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -628,13 +900,17 @@ bool make_q_map(CUtensorMap* m, const void* base, int Hq, int T, int L, int G) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int G>
-cudaError_t launch_memory_t(const Attend& a, int max_splits, cudaStream_t s) {
-  CUtensorMap tm_q, tm_kv;
-  if (!make_q_map(&tm_q, a.q, a.H * G, a.T, a.L, G) ||
-      !make_kv_map(&tm_kv, a.mem_kv, (uint64_t)a.NG * a.L * 2 * a.H * a.M_max))
+template <int G, bool BLOCK>
+cudaError_t launch_tiles_t(const Attend& a, int max_splits, cudaStream_t s) {
+  CUtensorMap tm_q, tm_kv, tm_pages;
+  if (!make_q_map(&tm_q, a.q, a.H * G, a.T, a.L, G)) return cudaErrorInvalidValue;
+  tm_kv = tm_pages = tm_q;  // (whichever is not read)
+  if (a.NG > 0 && !make_kv_map(&tm_kv, a.mem_kv, (uint64_t)a.NG * a.L * 2 * a.H * a.M_max, kBox))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(memory_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTc);
+  if (BLOCK && !make_kv_map(&tm_pages, a.pages, ((uint64_t)a.L * a.NP * 2 * a.H) << a.log2_page,
+                            std::min(kBox, 1 << a.log2_page)))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(tile_kernel<G, BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(msa::sm_count(), 1, 1);
@@ -646,17 +922,26 @@ cudaError_t launch_memory_t(const Attend& a, int max_splits, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, memory_kernel<G>, tm_q, tm_kv, a, max_splits);
+  return cudaLaunchKernelEx(&cfg, tile_kernel<G, BLOCK>, tm_q, tm_kv, tm_pages, a, max_splits);
 }
 
 }  // namespace
 
 cudaError_t launch_memory(const Attend& a, int max_splits, cudaStream_t s) {
   switch (a.G) {
-    case 1: return launch_memory_t<1>(a, max_splits, s);
-    case 2: return launch_memory_t<2>(a, max_splits, s);
-    case 4: return launch_memory_t<4>(a, max_splits, s);
-    default: return launch_memory_t<8>(a, max_splits, s);
+    case 1: return launch_tiles_t<1, false>(a, max_splits, s);
+    case 2: return launch_tiles_t<2, false>(a, max_splits, s);
+    case 4: return launch_tiles_t<4, false>(a, max_splits, s);
+    default: return launch_tiles_t<8, false>(a, max_splits, s);
+  }
+}
+
+cudaError_t launch_blocks(const Attend& a, cudaStream_t s) {
+  switch (a.G) {
+    case 1: return launch_tiles_t<1, true>(a, 1, s);
+    case 2: return launch_tiles_t<2, true>(a, 1, s);
+    case 4: return launch_tiles_t<4, true>(a, 1, s);
+    default: return launch_tiles_t<8, true>(a, 1, s);
   }
 }
 
