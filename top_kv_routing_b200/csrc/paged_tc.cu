@@ -18,11 +18,16 @@
 //   warp 9               TMA: the unit's query rows (4D box), then 128-key tiles of K and V in
 //                        the order the MMAs use them, through a ring of 32 KB slots (memory
 //                        tiles as 64-row boxes, page tiles as one box per page, a lane each);
-//   warp 8               MMA issue for two streams a and b: S = Q K^T (queries from shared
+//   warp 8, one thread   MMA issue for two streams a and b: S = Q K^T (queries from shared
 //                        memory, M = N = 128), O += P V (weights from tensor memory, written
 //                        over their scores; V read MN-major from its rows).  PV_a(j), S_a(j+1),
 //                        PV_b(j), S_b(j+1), ...: while one stream's softmax runs, the tensor
-//                        cores work for the other;
+//                        cores work for the other.  A PV starts on the weights of the first 64
+//                        keys while the softmax computes those of the others;
+//   warp 10              prepares value tiles before their PV: rows past the last valid one,
+//                        which may hold anything, are zeroed, and values that are not finite
+//                        taken out where some rows must not see them;
+//   warp 11              works out the units ahead of everyone else (a ring of kUnits);
 //   warps 0..3, 4..7     the softmax of stream a and of stream b: a thread per row, with the
 //                        registers that warps 8..11 give up.  A running maximum that is raised
 //                        (and O rescaled in tensor memory) only when a score exceeds it by more
@@ -58,18 +63,34 @@ constexpr int kHalf = 64;                 // dims of a 128-byte swizzled row
 constexpr int kHalfBytes = kTile * 128;   // 16 KB: 128 rows x 64 dims
 constexpr int kSlotBytes = 2 * kHalfBytes;  // one K or V tile, or one query tile
 constexpr int kSlots = 4;
-constexpr int kWarpsTc = 12;              // 0..7 softmax, 8 MMA, 9 TMA, 10 and 11 none
+constexpr int kUnits = 4;                 // units worked out ahead
+constexpr int kWarpsTc = 12;              // 0..7 softmax, 8 MMA, 9 TMA, 10 value tiles, 11 units
 constexpr int kThreadsTc = kWarpsTc * 32;
-// registers: 168 a thread at launch; 128 x 80 + 256 x 208 <= 384 x 168
-constexpr int kRegsIssue = 80, kRegsSoftmax = 208;
+// registers: 168 a thread at launch; 128 x 72 + 256 x 216 = 384 x 168
+constexpr int kRegsIssue = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreadsTc * 168, "register split");
 constexpr int kPolyOf8 = 2;               // of every 8 exponentials, those on the FMA pipe
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kValueWarp = 10;
 constexpr uint32_t kTmemCols = 512;       // S_a | S_b | O_a | O_b
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kHeadroom = 8.0f;         // log2 growth of a row's maximum tolerated before rescaling
 
 constexpr int kBadRing = 8;               // tiles whose page masks are kept (more than are in flight)
+
+// One unit as every role sees it.
+struct Unit {
+  int e, l, h;               // entry, layer, key head
+  int tok[2], n_tok[2];      // each stream's tokens
+  int t0[2], t1[2];          // each stream's key tiles [t0, t1)
+  int M, mt;                 // memory rows and tiles (the page tiles follow)
+  int n_loc;                 // page rows that some row sees
+  int lim0;                  // page rows that the first token sees (token i: i more, up to len)
+  int len;                   // page rows (clamped)
+  bool shared;               // the streams read the same key tiles
+  int64_t kv_row;            // row of key 0 in the memory tensor; values H * M_max further
+  int slot[2];               // partial slot
+  int poison;                // block form: values that are not finite were taken out of its tiles
+};
 
 // The batch in shared memory: an entry is a group (memory form) or a sequence (block form).
 struct TablesTc {
@@ -83,14 +104,14 @@ struct TablesTc {
   int splits;
   uint32_t tmem;
   int abort;
-  int poison[2];           // block form, by stream: units + 1 of its last one with values cleared
+  Unit units[kUnits];      // unit u of this CTA in place u % kUnits
   uint32_t bad[kBadRing];  // block form: per tile, its 16-row pieces without a usable page
 };
 
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kSlotBytes;
 constexpr int kOffBars = kOffRing + kSlots * kSlotBytes;
-constexpr int kOffTables = kOffBars + 256;
+constexpr int kOffTables = kOffBars + 384;
 constexpr int kSmemTc = kOffTables + (int)sizeof(TablesTc) + 1024;  // (+ alignment of the dynamic base)
 static_assert(kSmemTc <= 227 * 1024, "shared memory");
 
@@ -185,20 +206,6 @@ __device__ __forceinline__ void ex2_poly(f32x2 x2, float& y0, float& y1) {
   y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 
-// One unit as every role sees it.
-struct Unit {
-  int e, l, h;               // entry, layer, key head
-  int tok[2], n_tok[2];      // each stream's tokens
-  int t0[2], t1[2];          // each stream's key tiles [t0, t1)
-  int M, mt;                 // memory rows and tiles (the page tiles follow)
-  int n_loc;                 // page rows that some row sees
-  int lim0;                  // page rows that the first token sees (token i: i more, up to len)
-  int len;                   // page rows (clamped)
-  bool shared;               // the streams read the same key tiles
-  int64_t kv_row;            // row of key 0 in the memory tensor; values H * M_max further
-  int slot[2];               // partial slot
-};
-
 // Adds the values that are not finite of the page tiles that were cleared of them (those a row
 // of the pair does not see in full), as far as this row sees them, to its 32 dims from d0.
 __device__ __forceinline__ void add_not_finite(const Attend& a, const Unit& x, int seen, int d0, uint32_t (&o)[32]) {
@@ -225,13 +232,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   TablesTc& tb = *reinterpret_cast<TablesTc*>(smem + kOffTables);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint64_t* full = bars;                 // [kSlots] tile landed
-  uint64_t* empty = bars + kSlots;       // [kSlots] tile read by its MMAs
+  uint64_t* empty = bars + kSlots;       // [kSlots] tile read by its MMAs and passed by warp 10
   uint64_t* q_full = bars + 2 * kSlots;  // [2] the stream's queries landed
   uint64_t* q_empty = q_full + 2;        // [2] read by the stream's last score MMA of the unit
   uint64_t* s_ready = q_empty + 2;       // [2] scores in tensor memory (and the stream's PV before them done)
-  uint64_t* p_ready = s_ready + 2;       // [2] weights in tensor memory (4 warps)
-  uint64_t* o_done = p_ready + 2;        // [2] the stream's last PV of the unit done
-  uint64_t* drain = o_done + 2;
+  uint64_t* p_ready = s_ready + 2;       // [2][2] weights of keys 0..63, 64..127 in tensor memory (4 warps)
+  uint64_t* o_done = p_ready + 4;        // [2] the stream's last PV of the unit done
+  uint64_t* v_ready = o_done + 2;        // [kSlots] the n-th tile that warp 10 prepares (n % kSlots)
+  uint64_t* u_full = v_ready + kSlots;   // [kUnits] unit worked out
+  uint64_t* u_empty = u_full + kUnits;   // [kUnits] not needed any more (TMA, MMA, value, 8 softmax warps)
+  uint64_t* drain = u_empty + kUnits;
   volatile int* abort_flag = &tb.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem);
@@ -240,18 +250,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 2);
+      mbar_init(smem_u32(&v_ready[s]), 1);
+    }
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(smem_u32(&u_full[s]), 1);
+      mbar_init(smem_u32(&u_empty[s]), 11);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&q_full[x]), 1);
       mbar_init(smem_u32(&q_empty[x]), 1);
       mbar_init(smem_u32(&s_ready[x]), 1);
-      mbar_init(smem_u32(&p_ready[x]), 4);
+      mbar_init(smem_u32(&p_ready[2 * x]), 4);
+      mbar_init(smem_u32(&p_ready[2 * x + 1]), 4);
       mbar_init(smem_u32(&o_done[x]), 1);
     }
     mbar_init(smem_u32(drain), 1);
     tb.abort = 0;
-    tb.poison[0] = tb.poison[1] = 0;
     tb.most = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
@@ -371,6 +386,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     x.n_tok[0] = min(kTok, n - at);
     x.n_loc = x.lim0 = x.len = 0;
     x.slot[0] = x.slot[1] = s;
+    x.poison = 0;
     x.shared = BLOCK || n > kTok;
     if (BLOCK) {
       x.tok[1] = x.tok[0] + kTok;
@@ -409,7 +425,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     return !BLOCK || tile < x.mt ? min(kTile, x.M - tile * kTile) : min(kTile, x.n_loc - (tile - x.mt) * kTile);
   };
 
-  // (in each role's own branch: the compiler allocates what follows by it)
+  // a value tile that warp 10 prepares: rows past the last valid one within a 16-key step, or a
+  // page tile that some rows of the pair do not see in full
+  auto prepared = [&](const Unit& x, int tile) -> bool {
+    return (valid_keys(x, tile) & 15) != 0 || (BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0);
+  };
+  // unit un of this CTA (every lane of the caller's warp, or its one thread, waits)
+  auto unit_wait = [&](int un) -> bool { return mbar_wait(smem_u32(&u_full[un % kUnits]), (un / kUnits) & 1u, abort_flag); };
+
+  // (setmaxnreg in each role's own branch: the compiler allocates what follows by it)
   if (warp == kTmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // ---- loads: the warp walks together (a lane per page box), lane 0 arms and waits
@@ -499,8 +523,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       __syncwarp();
     };
-    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      const Unit x = unit_at(u);
+    int un = 0;
+    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
+      if (!__all_sync(0xffffffffu, unit_wait(un))) {
+        ok = false;
+        break;
+      }
+      const Unit x = tb.units[un % kUnits];
       const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
       // tile j of stream b is loaded for it alone
       auto own_b = [&](int j) { return j < n1 && (!x.shared || j >= n0); };
@@ -520,6 +549,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (own_b(j)) load(x, x.t0[1] + j, true);
         if (own_b(j + 1)) load(x, x.t0[1] + j + 1, false);
       }
+      if (lane == 0) mbar_arrive(smem_u32(&u_empty[un % kUnits]));
+      __syncwarp();
     }
     if (!ok) {
       // wait (bounded) for the copies in flight: the last kSlots loads and the last query tiles
@@ -535,159 +566,117 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
   } else if (warp == kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    // the warp waits together, one elected lane issues
-    const bool leader = elect_one();
-    constexpr uint32_t idesc_s = idesc_make(kRows, kTile, false);
-    constexpr uint32_t idesc_pv = idesc_make_bmn(kRows, kD);
-    bool ok = true, issued = false;
-    uint32_t it = 0;               // ring position of the next tile
-    uint32_t qn[2] = {0, 0};       // query tiles used per stream
-    uint32_t pn[2] = {0, 0};       // weight tiles used per stream
-    uint32_t kpos = 0, vpos = 0;   // (shared) ring positions of stream a's current K and V
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
-      if (ok) tc_fence_after();
-      return ok;
-    };
-    // Values that are not finite must not reach the rows that do not see them (0 x inf is NaN):
-    // they are cleared, and the unit is marked for each stream before its last PV (a stream is
-    // then still in this unit); its rows add what they see of them at the end.
-    bool cleared = false;
-    auto clear_not_finite = [&](uint32_t vt, int rows) {
-      bool any = false;
-      for (int i = lane; i < rows * 16; i += 32) {
-        const uint32_t at = vt + (uint32_t)((i & 8 ? kHalfBytes : 0) + (i >> 4) * 128 + (i & 7) * 16);
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(at)
-                     : "memory");
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u, bad = true;
-          if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0x0000FFFFu, bad = true;
-        }
-        if (bad)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
-        any |= bad;
-      }
-      if (__any_sync(0xffffffffu, any)) {
-        cleared = true;
-        fence_async_smem();
-        __syncwarp();
-      }
-    };
-    // scores of stream st over its key tile in ring position `pos`; `release`: the tile's last use
-    auto score = [&](int st, uint32_t pos, bool release, bool last) {
-      if (!ok) return;
-      if (!wait(&full[pos % kSlots], (pos / kSlots) & 1u)) return;
-      if (leader) {
-        const uint32_t kt = sbase + kOffRing + (pos % kSlots) * kSlotBytes;
-        const uint32_t qt = sbase + kOffQ + st * kSlotBytes;
+    if (elect_one()) {
+      // one thread waits and issues.  Descriptors: the low words carry the address (and the
+      // leading offset), the high words are the same for all tiles of a kind.
+      constexpr uint32_t idesc_s = idesc_make(kRows, kTile, false);
+      constexpr uint32_t idesc_pv = idesc_make_bmn(kRows, kD);
+      const uint64_t rows_desc = sw128_desc(sbase), cols_desc = sw128_desc_mn(sbase, kHalfBytes, 1024);
+      auto at = [](uint64_t desc, uint32_t bytes) -> uint64_t { return desc + (uint64_t)(bytes >> 4); };
+      bool ok = true, issued = false;
+      uint32_t it = 0;               // ring position of the next tile
+      uint32_t prep = 0;             // tiles that warp 10 prepared
+      uint32_t qn[2] = {0, 0};       // query tiles used per stream
+      uint32_t pn[2] = {0, 0};       // weight tiles used per stream
+      uint32_t kpos = 0, vpos = 0;   // (shared) ring positions of stream a's current K and V
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && mbar_wait(smem_u32(bar), parity, abort_flag);
+      };
+      auto landed = [&](uint32_t pos) { wait(&full[pos % kSlots], (pos / kSlots) & 1u); };
+      // scores of stream st over the key tile in ring position `pos` (landed); `release`: the
+      // tile's last use; `last`: the queries' last use
+      auto score = [&](int st, uint32_t pos, bool release, bool last) {
+        if (!ok) return;
+        const uint64_t kt = at(rows_desc, kOffRing + (pos % kSlots) * kSlotBytes);
+        const uint64_t qt = at(rows_desc, kOffQ + st * kSlotBytes);
         const uint32_t d = tmem_base + kColS + (uint32_t)(st * kTile);
 #pragma unroll
         for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint32_t off = (uint32_t)((ks >> 2) * kHalfBytes);
-          umma<false, false>(d, sw128_desc(qt + off) + (uint64_t)(2 * (ks & 3)),
-                             sw128_desc(kt + off) + (uint64_t)(2 * (ks & 3)), idesc_s, ks > 0 ? 1u : 0u);
+          const uint32_t off = (uint32_t)((ks >> 2) * kHalfBytes + (ks & 3) * 32);
+          umma<false, false>(d, at(qt, off), at(kt, off), idesc_s, ks > 0 ? 1u : 0u);
         }
         umma_commit<false>(smem_u32(&s_ready[st]));
         if (release) umma_commit<false>(smem_u32(&empty[pos % kSlots]));
         if (last) umma_commit<false>(smem_u32(&q_empty[st]));
-      }
-      issued = true;
-      __syncwarp();
-    };
-    auto weigh = [&](int st, uint32_t pos, int valid, bool first, bool release, bool last, bool check, int unit) {
-      if (!ok) return;
-      if (!wait(&p_ready[st], pn[st] & 1u)) return;
-      ++pn[st];
-      if (!wait(&full[pos % kSlots], (pos / kSlots) & 1u)) return;
-      const uint32_t vt = sbase + kOffRing + (pos % kSlots) * kSlotBytes;
-      const int n_ks = min(kTile, valid + 15) / 16;  // 16-key steps
-      if (valid < n_ks * 16) {  // rows past the last valid one may hold anything
-        for (int i = lane; i < (n_ks * 16 - valid) * 16; i += 32) {
-          const int row = valid + (i >> 4), c16 = i & 15;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (uint32_t)((c16 >> 3) * kHalfBytes + row * 128 +
-                                                                               (((c16 & 7) ^ (row & 7)) << 4))),
-                       "r"(0u)
-                       : "memory");
-        }
-        fence_async_smem();
-        __syncwarp();
-      }
-      if (BLOCK && check) clear_not_finite(vt, n_ks * 16);
-      if (BLOCK && last && cleared) {
-        if (lane == 0) tb.poison[st] = unit + 1;
-        __threadfence_block();
-        __syncwarp();
-      }
-      if (leader) {
-        const uint32_t p = tmem_base + kColS + (uint32_t)(st * kTile);
-        const uint32_t d = tmem_base + kColO + (uint32_t)(st * kTile);
-        for (int ks = 0; ks < n_ks; ++ks)
-          umma_ts(d, p + (uint32_t)(8 * ks), sw128_desc_mn(vt + (uint32_t)(ks * 2048), kHalfBytes, 1024), idesc_pv,
-                  (!first || ks > 0) ? 1u : 0u);
-        if (release) umma_commit<false>(smem_u32(&empty[pos % kSlots]));
-        if (last) umma_commit<false>(smem_u32(&o_done[st]));
-      }
-      __syncwarp();
-    };
-    int64_t u = blockIdx.x;
-    for (int un = 0; u < n_units && ok; u += gridDim.x, ++un) {
-      const Unit x = unit_at(u);
-      cleared = false;
-      const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
-      auto with_a = [&](int j) { return x.shared && j < n0; };  // stream b reads stream a's tile j
-      auto with_b = [&](int j) { return x.shared && j < n1; };
-      // a page tile that some rows of the pair do not see in full
-      auto edge = [&](int tile) { return BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0; };
-      auto q_wait = [&](int st) {
-        if (ok && wait(&q_full[st], qn[st] & 1u)) ++qn[st];
+        issued = true;
       };
-      if (n0 > 0) {
-        q_wait(0);
-        kpos = it++;
-        score(0, kpos, !with_b(0), n0 == 1);
-      }
-      if (n1 > 0) {
-        q_wait(1);
-        const uint32_t pos = with_a(0) ? kpos : it++;
-        score(1, pos, true, n1 == 1);
-      }
-      for (int j = 0; j < max(n0, n1) && ok; ++j) {
-        if (j < n0) {
-          vpos = it++;
-          weigh(0, vpos, valid_keys(x, x.t0[0] + j), j == 0, !with_b(j), j + 1 == n0, edge(x.t0[0] + j), un);
-          if (j + 1 < n0) {
-            kpos = it++;
-            score(0, kpos, !with_b(j + 1), j + 2 == n0);
+      // O += P V of stream st over the value tile in ring position `pos` (ready): 16-key steps
+      // 4 h .. 4 h + 3 as far as there are keys
+      auto weigh = [&](int st, uint32_t pos, int h, int n_ks, bool first) {
+        wait(&p_ready[2 * st + h], pn[st] & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t vt = at(cols_desc, kOffRing + (pos % kSlots) * kSlotBytes + h * 4 * 2048);
+        const uint32_t p = tmem_base + kColS + (uint32_t)(st * kTile + h * 32);
+        const uint32_t d = tmem_base + kColO + (uint32_t)(st * kTile);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          if (4 * h + ks < n_ks)
+            umma_ts(d, p + (uint32_t)(8 * ks), at(vt, ks * 2048), idesc_pv, (!first || 4 * h + ks > 0) ? 1u : 0u);
+      };
+      int un = 0;
+      for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
+        wait(&u_full[un % kUnits], (un / kUnits) & 1u);
+        if (!ok) break;
+        const Unit& x = tb.units[un % kUnits];
+        const int t0a = x.t0[0], t0b = x.t0[1];
+        const int n0 = x.t1[0] - t0a, n1 = x.t1[1] - t0b;
+        const bool shared = x.shared;
+        auto with_a = [&](int j) { return shared && j < n0; };  // stream b reads stream a's tile j
+        auto with_b = [&](int j) { return shared && j < n1; };
+        // PV of tile j of stream st, then the scores of its tile j + 1
+        auto step = [&](int st, int j, int tile, int n, bool own, bool v_release, bool k_own, bool k_release) {
+          const uint32_t pv = own ? it++ : vpos;
+          if (st == 0) vpos = pv;
+          const bool more = j + 1 < n;
+          uint32_t pk = kpos;
+          if (more && k_own) pk = it++;
+          if (st == 0) kpos = pk;
+          const int n_ks = (valid_keys(x, tile) + 15) >> 4;
+          if (own) {
+            landed(pv);
+            if (prepared(x, tile)) {
+              wait(&v_ready[prep % kSlots], (prep / kSlots) & 1u);
+              ++prep;
+            }
           }
+          weigh(st, pv, 0, n_ks, j == 0);
+          if (more) landed(pk);
+          weigh(st, pv, 1, n_ks, j == 0);
+          ++pn[st];
+          if (!ok) return;
+          if (v_release) umma_commit<false>(smem_u32(&empty[pv % kSlots]));
+          if (!more) umma_commit<false>(smem_u32(&o_done[st]));
+          if (more) score(st, pk, k_release, j + 2 == n);
+        };
+        if (n0 > 0) {
+          wait(&q_full[0], qn[0]++ & 1u);
+          kpos = it++;
+          landed(kpos);
+          score(0, kpos, !with_b(0), n0 == 1);
         }
-        if (j < n1) {
-          const bool alone = !with_a(j);
-          const uint32_t pv = alone ? it++ : vpos;
-          weigh(1, pv, valid_keys(x, x.t0[1] + j), j == 0, true, j + 1 == n1, alone && edge(x.t0[1] + j), un);
-          if (j + 1 < n1) {
-            const uint32_t pk = with_a(j + 1) ? kpos : it++;
-            score(1, pk, true, j + 2 == n1);
-          }
+        if (n1 > 0) {
+          wait(&q_full[1], qn[1]++ & 1u);
+          const uint32_t pos = with_a(0) ? kpos : it++;
+          landed(pos);
+          score(1, pos, true, n1 == 1);
         }
+        for (int j = 0; j < max(n0, n1) && ok; ++j) {
+          if (j < n0) step(0, j, t0a + j, n0, true, !with_b(j), true, !with_b(j + 1));
+          if (j < n1) step(1, j, t0b + j, n1, !with_a(j), true, !with_a(j + 1), true);
+        }
+        mbar_arrive(smem_u32(&u_empty[un % kUnits]));
       }
-    }
-    if (!ok) {
-      if (lane == 0) {
+      if (!ok) {
         *abort_flag = 1;
         msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
-      }
-      if (issued) {
-        if (leader) umma_commit<false>(smem_u32(drain));
-        __syncwarp();
-        mbar_drain(smem_u32(drain), 0u);
+        if (issued) {
+          umma_commit<false>(smem_u32(drain));
+          mbar_drain(smem_u32(drain), 0u);
+        }
       }
     }
+    __syncwarp();
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ---- softmax: stream st, thread = row (TMEM lane)
@@ -704,13 +693,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     bool ok = true;
     int64_t u = blockIdx.x;
     for (int un = 0; u < n_units && ok; u += gridDim.x, ++un) {
-      const Unit x = unit_at(u);
-      const int t0 = x.t0[st], n = x.t1[st] - t0;
+      if (!__all_sync(0xffffffffu, unit_wait(un))) {
+        ok = false;
+        break;
+      }
+      const Unit& x = tb.units[un % kUnits];
+      const int t0 = x.t0[st], n = x.t1[st] - t0, M = x.M, mt = x.mt;
       const int tk = r / G;                     // this row's token in its row tile
       const bool mine = tk < x.n_tok[st];
       const int64_t row = x.slot[st] * all_rows + ((int64_t)x.l * a.T + x.tok[st] + tk) * Hq + x.h * G + r % G;
       // page rows that this row sees
       const int seen = BLOCK ? max(0, min(x.lim0 + st * kTok + tk, x.len)) : 0;
+      const uint32_t tiles_after = tiles + (BLOCK ? max(x.t1[0], x.t1[1]) : 0);
       float m = -INFINITY;
       float sum = 0.f;
       for (int j = 0; j < n; ++j) {
@@ -724,8 +718,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
         tmem_wait_ld();
-        const bool page = BLOCK && t0 + j >= x.mt;
-        const int valid = page ? seen - (t0 + j - x.mt) * kTile : x.M - (t0 + j) * kTile;
+        const bool page = BLOCK && t0 + j >= mt;
+        const int valid = page ? seen - (t0 + j - mt) * kTile : M - (t0 + j) * kTile;
         const uint32_t bad = BLOCK ? *const_cast<volatile uint32_t*>(&tb.bad[(tiles + j) % kBadRing]) : 0u;
         bool plain = valid >= kTile && bad == 0u;
         if (!__all_sync(0xffffffffu, plain)) {
@@ -788,18 +782,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
               pw[e] = msa::float2_to_bf16x2(p0, p1);
             }
             tmem_st32(s_col + 32 * c, pw);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * st + c]));
           }
         };
         if (__all_sync(0xffffffffu, plain)) weights(Yes{}); else weights(No{});
         float s0, s1;
         unpack2(add2(add[0], add[1]), s0, s1);
         sum += s0 + s1;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_ready[st]));
       }
-      if (BLOCK) tiles += max(x.t1[0], x.t1[1]);
+      tiles = tiles_after;
       if (!ok) break;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no key seen: output 0; a NaN sum is kept)
       if (n > 0) {
@@ -810,7 +804,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         ++on;
         tc_fence_after();
       }
-      const bool poisoned = BLOCK && *const_cast<volatile int*>(&tb.poison[st]) == un + 1;
+      const bool poisoned = BLOCK && *const_cast<volatile int*>(&tb.units[un % kUnits].poison) != 0;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -840,13 +834,121 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       tc_fence_before();  // (O is read: the next unit's first PV may overwrite it)
       if (!BLOCK && mine) stat[row] = make_float2(m, sum);  // (no tiles: -inf and 0)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&u_empty[un % kUnits]));
     }
     if (!ok) {
       *abort_flag = 1;
       if (lane == 0) msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
     }
+  } else if (warp == kValueWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    // ---- value tiles.  The warp passes every tile of the ring in order (and no slot is filled
+    // again before), so that the phases it waits for are never ambiguous.
+    bool ok = true;
+    uint32_t it = 0, prep = 0;
+    auto pass = [&](int tiles, auto prepare) {
+      for (int i = 0; i < tiles && ok; ++i, ++it) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[it % kSlots]), (it / kSlots) & 1u, abort_flag))) {
+          ok = false;
+          return;
+        }
+        prepare(sbase + kOffRing + (it % kSlots) * kSlotBytes);
+        if (lane == 0) mbar_arrive(smem_u32(&empty[it % kSlots]));
+        __syncwarp();
+      }
+    };
+    auto keys = [&](bool any) { pass(any, [](uint32_t) {}); };
+    auto prepare_values = [&](const Unit& x, int tile, uint32_t vt, int un) {
+      if (!prepared(x, tile)) return;
+      const int valid = valid_keys(x, tile), rows = (valid + 15) & ~15;
+      for (int i = lane; i < (rows - valid) * 16; i += 32) {
+        const int row = valid + (i >> 4), c16 = i & 15;
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (uint32_t)((c16 >> 3) * kHalfBytes + row * 128 +
+                                                                             (((c16 & 7) ^ (row & 7)) << 4))),
+                     "r"(0u)
+                     : "memory");
+      }
+      __syncwarp();
+      // Values that are not finite must not reach the rows that do not see them (0 x inf is NaN):
+      // they are taken out, and the unit's rows add what they see of them at the end.
+      if (BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0) {
+        bool any = false;
+        for (int i0 = 0; i0 < rows; i0 += 16) {  // 16 rows: 8 pieces of 16 bytes a lane
+          uint32_t w[8][4];
+          const uint32_t from = vt + (uint32_t)(i0 * 128 + lane * 16);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[e][0]), "=r"(w[e][1]), "=r"(w[e][2]), "=r"(w[e][3])
+                         : "r"(from + (uint32_t)((e >> 2) * kHalfBytes + (e & 3) * 512))
+                         : "memory");
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            bool bad = false;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              if ((w[e][v] & 0x7F80u) == 0x7F80u) w[e][v] &= 0xFFFF0000u, bad = true;
+              if ((w[e][v] & 0x7F800000u) == 0x7F800000u) w[e][v] &= 0x0000FFFFu, bad = true;
+            }
+            if (bad)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               from + (uint32_t)((e >> 2) * kHalfBytes + (e & 3) * 512)),
+                           "r"(w[e][0]), "r"(w[e][1]), "r"(w[e][2]), "r"(w[e][3])
+                           : "memory");
+            any |= bad;
+          }
+        }
+        if (__any_sync(0xffffffffu, any) && lane == 0) *const_cast<volatile int*>(&tb.units[un % kUnits].poison) = 1;
+      }
+      __threadfence_block();
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&v_ready[prep % kSlots]));
+      ++prep;
+    };
+    int un = 0;
+    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
+      if (!__all_sync(0xffffffffu, unit_wait(un))) {
+        ok = false;
+        break;
+      }
+      const Unit& x = tb.units[un % kUnits];
+      const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
+      auto own_b = [&](int j) { return j < n1 && (!x.shared || j >= n0); };
+      // (the order of the loads: first key tiles, then value tile j and key tile j + 1 by stream)
+      keys(n0 > 0);
+      keys(own_b(0));
+      for (int j = 0; j < max(n0, n1) && ok; ++j) {
+        pass(j < n0, [&](uint32_t vt) { prepare_values(x, x.t0[0] + j, vt, un); });
+        keys(j + 1 < n0);
+        pass(own_b(j), [&](uint32_t vt) { prepare_values(x, x.t0[1] + j, vt, un); });
+        keys(own_b(j + 1));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&u_empty[un % kUnits]));
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    // ---- units
+    if (lane == 0) {
+      int un = 0;
+      for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++un) {
+        const Unit x = unit_at(u);
+        if (!mbar_wait(smem_u32(&u_empty[un % kUnits]), ((un / kUnits) & 1u) ^ 1u, abort_flag)) {
+          *abort_flag = 1;
+          msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
+          break;
+        }
+        tb.units[un % kUnits] = x;
+        mbar_arrive(smem_u32(&u_full[un % kUnits]));
+      }
+    }
+    __syncwarp();
   }
 
   tc_fence_before();
