@@ -89,25 +89,6 @@ struct AppendArgs {
   RopeFreq rf;
 };
 
-// The sequence of token t by a 32-way search over the (non-decreasing) offsets: the last b
-// with off[b] <= t; -1 when off[0] > t.  Always in [-1, B), whatever the offsets hold.
-__device__ __forceinline__ int find_sequence(const int32_t* __restrict__ off, int B, int t, int lane) {
-  int lo = 0, n = B;
-  bool any = false;
-  while (true) {
-    const int step = (n + 31) >> 5;
-    const int idx = lo + lane * step;
-    const bool le = idx < lo + n && off[idx] <= t;
-    const unsigned m = __ballot_sync(0xffffffffu, le);
-    if (m == 0u) return any ? lo : -1;  // (later rounds: off[lo] <= t was seen, so m != 0)
-    const int c = 31 - __clz(m);
-    any = true;
-    n = min(step, lo + n - (lo + c * step));
-    lo += c * step;
-    if (step == 1) return lo;
-  }
-}
-
 struct Eight {
   float x[8];
 };
@@ -172,7 +153,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
   if (warp < TOK) {
     const int t = t0 + warp;
-    int b = t < a.T ? find_sequence(a.off, a.B, t, lane) : -1;
+    int b = t < a.T ? find_last(a.off, a.B, t, lane) : -1;
     int b0 = 0, n = 0;
     if (b >= 0 && (!sequence_tokens(a.off, b, a.T, b0, n) || t < b0 || t >= b0 + n)) b = -1;
     int64_t row = -1;

@@ -113,4 +113,24 @@ __device__ __forceinline__ bool group_tokens(const Attend& a, int g, int& lo, in
   return ok;
 }
 
+// The last b in [0, B) with off[b] <= t, by a 32-way search over the (non-decreasing) offsets
+// (the sequence of token t, the group of sequence t); -1 when off[0] > t.  Always in [-1, B),
+// whatever the offsets hold.
+__device__ __forceinline__ int find_last(const int32_t* __restrict__ off, int B, int t, int lane) {
+  int lo = 0, n = B;
+  bool any = false;
+  while (true) {
+    const int step = (n + 31) >> 5;
+    const int idx = lo + lane * step;
+    const bool le = idx < lo + n && off[idx] <= t;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    if (m == 0u) return any ? lo : -1;  // (later rounds: off[lo] <= t was seen, so m != 0)
+    const int c = 31 - __clz(m);
+    any = true;
+    n = min(step, lo + n - (lo + c * step));
+    lo += c * step;
+    if (step == 1) return lo;
+  }
+}
+
 }  // namespace paged

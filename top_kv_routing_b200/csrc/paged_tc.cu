@@ -15,19 +15,21 @@
 // 推理全流程.
 //
 // Persistent CTAs (one per SM) of 384 threads walk the units:
-//   warp 9               TMA: the unit's query rows (4D box), then 128-key tiles of K and V in
-//                        the order the MMAs use them, through a ring of 32 KB slots (memory
-//                        tiles as 64-row boxes, page tiles as one box per page, a lane each);
+//   warp 9               TMA: 128-key tiles of K and V in the order the MMAs use them, through a
+//                        ring of 32 KB slots (memory tiles as 64-row boxes, page tiles as one
+//                        box per page, a lane each);
 //   warp 8, one thread   MMA issue for two streams a and b: S = Q K^T (queries from shared
 //                        memory, M = N = 128), O += P V (weights from tensor memory, written
 //                        over their scores; V read MN-major from its rows).  PV_a(j), S_a(j+1),
 //                        PV_b(j), S_b(j+1), ...: while one stream's softmax runs, the tensor
-//                        cores work for the other.  A PV starts on the weights of the first 64
+//                        cores work for the other; the next unit's first scores go
+//                        before stream b's last PV.  A PV starts on the weights of the first 64
 //                        keys while the softmax computes those of the others;
 //   warp 10              prepares value tiles before their PV: rows past the last valid one,
 //                        which may hold anything, are zeroed, and values that are not finite
 //                        taken out where some rows must not see them;
-//   warp 11              works out the units ahead of everyone else (a ring of kUnits);
+//   warp 11              works out the units ahead of everyone else (a ring of kUnits), and loads
+//                        their query rows (4D boxes);
 //   warps 0..3, 4..7     the softmax of stream a and of stream b: a thread per row, with the
 //                        registers that warps 8..11 give up.  A running maximum that is raised
 //                        (and O rescaled in tensor memory) only when a score exceeds it by more
@@ -35,11 +37,6 @@
 //                        the row sum takes them unrounded).
 // Streams a and b are the two row tiles of the pair over the same keys.  A group of at most
 // one row tile gives both streams the same rows and each half of the unit's keys instead.
-//
-// The exponentials bound the softmax: 2 x 16,384 per tile pair at 16 a clock take as long as
-// its MMAs (2,048 clocks), so kPolyOf8 of every 8 are computed on the FMA pipe instead: round x
-// to an integer n by the 1.5 x 2^23 addition, a minimax polynomial of degree 4 for 2^(x - n) on
-// [-1/2, 1/2] (Remez exchange, relative error 2.6e-6), n added to the exponent bits.
 //
 // S_x(j + 1) is issued after PV_x(j), so its completion also says that O_x is stable: the
 // softmax rescales it without another wait.  Key rows past the last valid one are zeroed in
@@ -62,14 +59,13 @@ constexpr int kBox = 64;                  // keys of a TMA box
 constexpr int kHalf = 64;                 // dims of a 128-byte swizzled row
 constexpr int kHalfBytes = kTile * 128;   // 16 KB: 128 rows x 64 dims
 constexpr int kSlotBytes = 2 * kHalfBytes;  // one K or V tile, or one query tile
-constexpr int kSlots = 4;
+constexpr int kSlots = 5;
 constexpr int kUnits = 4;                 // units worked out ahead
 constexpr int kWarpsTc = 12;              // 0..7 softmax, 8 MMA, 9 TMA, 10 value tiles, 11 units
 constexpr int kThreadsTc = kWarpsTc * 32;
 // registers: 168 a thread at launch; 128 x 72 + 256 x 216 = 384 x 168
 constexpr int kRegsIssue = 72, kRegsSoftmax = 216;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreadsTc * 168, "register split");
-constexpr int kPolyOf8 = 2;               // of every 8 exponentials, those on the FMA pipe
 constexpr int kMmaWarp = 8, kTmaWarp = 9, kValueWarp = 10;
 constexpr uint32_t kTmemCols = 512;       // S_a | S_b | O_a | O_b
 constexpr uint32_t kColS = 0, kColO = 256;
@@ -92,14 +88,11 @@ struct Unit {
   int poison;                // block form: values that are not finite were taken out of its tiles
 };
 
-// The batch in shared memory: an entry is a group (memory form) or a sequence (block form).
+// Shared variables.  An entry is a group (memory form) or a sequence (block form).
+constexpr int kBlocks = kMaxSeqs / 32;
+static_assert(kBlocks <= 32, "a lane per block of entries");
 struct TablesTc {
-  int scan[kMaxSeqs + 1];  // row-tile pairs of the entries before
-  int lo[kMaxSeqs];        // first token
-  int n[kMaxSeqs];         // tokens
-  int len[kMaxSeqs];       // block form: page rows, as given
-  int grp[kMaxSeqs];       // block form: group, or -1
-  int warp_sum[kWarpsTc];
+  int scan[kBlocks + 1];   // row-tile pairs of the entries before each 32
   int most;                // memory form: most key tiles of any (group, layer)
   int splits;
   uint32_t tmem;
@@ -151,13 +144,6 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&x)[8]) {
                : "memory");
 }
 
-struct Yes {
-  static constexpr bool value = true;
-};
-struct No {
-  static constexpr bool value = false;
-};
-
 // Packed pairs of fp32 (two registers).
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float lo, float hi) {
@@ -185,39 +171,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// 2^x for two finite x <= 126 on the FMA pipe (below 2^-125: 2^-125): n = round(x), a minimax
-// polynomial for 2^(x - n) on [-1/2, 1/2], n added to the exponent.
-__device__ __forceinline__ void ex2_poly(f32x2 x2, float& y0, float& y1) {
-  float x0, x1;
-  unpack2(x2, x0, x1);
-  x2 = pack2(fmaxf(x0, -125.f), fmaxf(x1, -125.f));
-  const f32x2 t = add2(x2, pack2(12582912.f, 12582912.f));
-  const f32x2 n = add2(t, pack2(-12582912.f, -12582912.f));
-  const f32x2 f = fma2(n, pack2(-1.f, -1.f), x2);
-  f32x2 p = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
-                 pack2(0.05591785907745361f, 0.05591785907745361f));
-  p = fma2(p, f, pack2(0.240247443318367f, 0.240247443318367f));
-  p = fma2(p, f, pack2(0.6931217908859253f, 0.6931217908859253f));
-  p = fma2(p, f, pack2(0.9999992847442627f, 0.9999992847442627f));
-  float p0, p1, t0, t1;
-  unpack2(p, p0, p1);
-  unpack2(t, t0, t1);
-  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
-}
-
 // Adds the values that are not finite of the page tiles that were cleared of them (those a row
-// of the pair does not see in full), as far as this row sees them, to its 32 dims from d0.
-__device__ __forceinline__ void add_not_finite(const Attend& a, const Unit& x, int seen, int d0, uint32_t (&o)[32]) {
+// of the pair does not see in full), as far as this row sees them, to its stored output.
+__device__ __noinline__ void add_not_finite(const Attend& a, const Unit& x, int seen, __nv_bfloat16* out) {
   const int page = 1 << a.log2_page;
-#pragma unroll 1
   for (int k = max(0, x.lim0) / kTile * kTile; k < seen; ++k) {
     const int id = a.page_table[(int64_t)x.e * a.max_pages + (k >> a.log2_page)];
     if (id < 0 || id >= a.NP) continue;
     const int64_t row = ((((((int64_t)x.l * a.NP + id) * 2 + 1) * a.H + x.h)) << a.log2_page) + (k & (page - 1));
-    for (int e = 0; e < 32; ++e) {
-      const float v = __bfloat162float(a.pages[row * kD + d0 + e]);
-      if (!(fabsf(v) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + v);
+    for (int e = 0; e < kD; ++e) {
+      const float v = __bfloat162float(a.pages[row * kD + e]);
+      if (!(fabsf(v) < INFINITY)) out[e] = __float2bfloat16(__bfloat162float(out[e]) + v);
     }
   }
 }
@@ -278,66 +242,53 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   wait_for_earlier_kernels();
   let_next_kernel_start();
 
-  // ---- tables: tokens and row-tile pairs of every entry
-  const int n_entries = BLOCK ? a.B : a.NG;
+  // ---- the batch: row-tile pairs, most key tiles
+  const int n_entries = BLOCK ? a.B : a.NG, n_blocks = (n_entries + 31) / 32;
   const int64_t cap = (int64_t)a.max_pages << a.log2_page;
   const bool groups_ok = group_offsets_usable(a, tid, kThreadsTc);  // (a barrier for all threads)
   if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+  // tokens of entry e; false where they are unusable
+  auto entry_tokens = [&](int e, int& lo, int& n) -> bool {
+    if (BLOCK) return sequence_tokens(a.q_offsets, e, a.T, lo, n);
+    lo = n = 0;
+    return groups_ok && group_tokens(a, e, lo, n);
+  };
+  auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
+  for (int k = warp; k < n_blocks; k += kWarpsTc) {
+    const int e = 32 * k + lane;
+    int lo = 0, n = 0;
+    if (e < n_entries && !entry_tokens(e, lo, n) && BLOCK && blockIdx.x == 0)
+      msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+    if (BLOCK && blockIdx.x == 0 && n > 0 && a.seq_len[e] > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
+    const int sum = __reduce_add_sync(0xffffffffu, pairs_of(n));
+    if (lane == 0) tb.scan[k] = sum;
+  }
   {
-    constexpr int kPer = (kMaxSeqs + kThreadsTc - 1) / kThreadsTc;
-    int v[kPer], sum = 0, most = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      v[i] = sum;
-      if (e < n_entries) {
-        int lo = 0, n = 0;
-        if (BLOCK) {
-          if (!sequence_tokens(a.q_offsets, e, a.T, lo, n) && blockIdx.x == 0)
-            msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-          const int len = a.seq_len[e];
-          if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
-          tb.len[e] = len;
-          tb.grp[e] = -1;
-        } else if (!groups_ok || !group_tokens(a, e, lo, n)) {
-          n = 0;
-        }
-        tb.lo[e] = lo;
-        tb.n[e] = n;
-        sum += (n + 2 * kTok - 1) / (2 * kTok);
-      }
-    }
+    int most = 0;
     for (int i = tid; i < a.NG * a.L; i += kThreadsTc) most = max(most, a.mem_len[i]);
     if (most > a.M_max) {
       if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
       most = a.M_max;
     }
     most = __reduce_max_sync(0xffffffffu, most);
-    int inc = sum;
+    if (lane == 0) atomicMax(&tb.most, (most + kTile - 1) / kTile);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {  // sums before each block
+    const int v = lane < n_blocks ? tb.scan[lane] : 0;
+    int inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
-    if (lane == 31) tb.warp_sum[warp] = inc;
-    if (lane == 0) atomicMax(&tb.most, (most + kTile - 1) / kTile);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int base = inc - sum;
-    for (int w = 0; w < warp; ++w) base += tb.warp_sum[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = tid * kPer + i;
-      if (e < n_entries) tb.scan[e] = base + v[i];
-    }
-    if (tid == kThreadsTc - 1) tb.scan[n_entries] = base + sum;
+    tb.scan[lane] = inc - v;
+    if (lane == 31) tb.scan[32] = inc;
   }
-  if (BLOCK && groups_ok)
-    for (int g = warp; g < a.NG; g += kWarpsTc)
-      for (int b = a.group_offsets[g] + lane; b < a.group_offsets[g + 1]; b += 32) tb.grp[b] = g;
   __syncthreads();
-  const int pairs = tb.scan[n_entries];
+  const int pairs = tb.scan[kBlocks];
   if (tid == 0) {
     int best = 1;
     if (!BLOCK) {
@@ -360,6 +311,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   const uint32_t tmem_base = tb.tmem;
   const int64_t n_units = (int64_t)pairs * LH * splits;
 
+  // the unit (the lanes of one warp together)
   auto unit_at = [&](int64_t u) -> Unit {
     Unit x;
     // memory form: pairs run fastest (CTAs at work together read the same keys); block form:
@@ -370,19 +322,34 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int lh = BLOCK ? (int)(u - rest * LH) : (int)(rest / splits);
     x.l = lh / a.H;
     x.h = lh - x.l * a.H;
-    int lo = 0, hi = n_entries;  // scan[lo] <= pair < scan[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (tb.scan[mid] <= pair) lo = mid; else hi = mid;
+    // the entry: its block of 32, then a scan over the block
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, lane < n_blocks && tb.scan[lane] <= pair));
+    const int e = 32 * k + lane;
+    int lo = 0, n = 0;
+    if (e < n_entries) entry_tokens(e, lo, n);
+    int before = pairs_of(n);
+    const int own_pairs = before;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
     }
-    x.e = lo;
-    const int g = BLOCK ? tb.grp[lo] : lo;
+    before += tb.scan[k] - own_pairs;
+    const int from = 31 - __clz(__ballot_sync(0xffffffffu, e < n_entries && before <= pair));
+    x.e = 32 * k + from;
+    lo = __shfl_sync(0xffffffffu, lo, from);
+    n = __shfl_sync(0xffffffffu, n, from);
+    const int at = (pair - __shfl_sync(0xffffffffu, before, from)) * 2 * kTok;
+    int g = x.e;
+    if (BLOCK) {
+      g = a.NG > 0 && groups_ok ? find_last(a.group_offsets, a.NG, x.e, lane) : -1;
+      if (g >= 0 && x.e >= a.group_offsets[g + 1]) g = -1;
+    }
     const int64_t gl = (int64_t)g * a.L + x.l;
     x.M = g < 0 ? 0 : max(0, min(a.M_max, __ldg(a.mem_len + gl)));
     x.kv_row = (gl * 2 * a.H + x.h) * a.M_max;
     x.mt = (x.M + kTile - 1) / kTile;
-    const int at = (pair - tb.scan[lo]) * 2 * kTok, n = tb.n[lo];
-    x.tok[0] = tb.lo[lo] + at;
+    x.tok[0] = lo + at;
     x.n_tok[0] = min(kTok, n - at);
     x.n_loc = x.lim0 = x.len = 0;
     x.slot[0] = x.slot[1] = s;
@@ -391,8 +358,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (BLOCK) {
       x.tok[1] = x.tok[0] + kTok;
       x.n_tok[1] = max(0, min(kTok, n - at - kTok));
-      x.len = (int)min((int64_t)max(tb.len[lo], 0), cap);
-      x.lim0 = max(tb.len[lo], 0) - n + at + 1;
+      const int len = max(a.seq_len[x.e], 0);
+      x.len = (int)min((int64_t)len, cap);
+      x.lim0 = len - n + at + 1;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int seen = max(0, min(x.lim0 + x.n_tok[0] - 1 + i * x.n_tok[1], x.len));
@@ -438,14 +406,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     // ---- loads: the warp walks together (a lane per page box), lane 0 arms and waits
     if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
       if (BLOCK) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_pages)) : "memory");
     }
     bool ok = true;
     uint32_t it = 0;                // ring position
     uint32_t tiles = 0;             // key tiles of the block form so far
-    uint32_t qn[2] = {0, 0};        // query tiles loaded per stream
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
       return ok;
@@ -510,57 +476,37 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (BLOCK && !is_v) ++tiles;
       __syncwarp();
     };
-    auto load_q = [&](const Unit& x, int st) {
-      if (!ok) return;
-      if (!wait(&q_empty[st], (qn[st] & 1u) ^ 1u)) return;
-      ++qn[st];
-      if (lane == 0) {
-        const uint32_t bar = smem_u32(&q_full[st]);
-        const uint32_t dst = sbase + kOffQ + st * kSlotBytes;
-        mbar_arrive_expect_tx(bar, kSlotBytes);
-        tma_load_4d(dst, &tm_q, bar, 0, x.h * G, x.tok[st], x.l);
-        tma_load_4d(dst + kHalfBytes, &tm_q, bar, kHalf, x.h * G, x.tok[st], x.l);
-      }
-      __syncwarp();
-    };
     int un = 0;
     for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
       if (!__all_sync(0xffffffffu, unit_wait(un))) {
         ok = false;
         break;
       }
-      const Unit x = tb.units[un % kUnits];
+      const Unit& x = tb.units[un % kUnits];
       const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
       // tile j of stream b is loaded for it alone
       auto own_b = [&](int j) { return j < n1 && (!x.shared || j >= n0); };
-      if (n0 > 0) {
-        load_q(x, 0);
-        load(x, x.t0[0], false);
-      }
-      if (n1 > 0) {
-        load_q(x, 1);
-        if (own_b(0)) load(x, x.t0[1], false);
-      }
-      for (int j = 0; j < max(n0, n1) && ok; ++j) {
-        if (j < n0) {
-          load(x, x.t0[0] + j, true);
-          if (j + 1 < n0) load(x, x.t0[0] + j + 1, false);
+      // the first key tiles (j = -1), then per j value tile j and key tile j + 1 of either stream
+#pragma unroll 1
+      for (int i = -2; i < 2 * max(n0, n1) && ok; ++i) {
+        const int st = i & 1, j = i >> 1;
+        auto own = [&](int k) { return st == 0 ? k < n0 : own_b(k); };
+#pragma unroll 1
+        for (int v = 1; v >= 0; --v) {
+          const int k = v ? j : j + 1;
+          if (k >= 0 && own(k)) load(x, x.t0[st] + k, v != 0);
         }
-        if (own_b(j)) load(x, x.t0[1] + j, true);
-        if (own_b(j + 1)) load(x, x.t0[1] + j + 1, false);
       }
       if (lane == 0) mbar_arrive(smem_u32(&u_empty[un % kUnits]));
       __syncwarp();
     }
     if (!ok) {
-      // wait (bounded) for the copies in flight: the last kSlots loads and the last query tiles
+      // wait (bounded) for the copies in flight: the last kSlots loads
       if (lane == 0) {
         *abort_flag = 1;
         msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
         for (uint32_t p = it > kSlots ? it - kSlots : 0; p < it; ++p)
           mbar_drain(smem_u32(&full[p % kSlots]), (p / kSlots) & 1u);
-        for (int st = 0; st < 2; ++st)
-          if (qn[st] > 0) mbar_drain(smem_u32(&q_full[st]), (qn[st] - 1) & 1u);
       }
       __syncwarp();
     }
@@ -614,13 +560,31 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (4 * h + ks < n_ks)
             umma_ts(d, p + (uint32_t)(8 * ks), at(vt, ks * 2048), idesc_pv, (!first || 4 * h + ks > 0) ? 1u : 0u);
       };
-      int un = 0;
-      for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
+      // stream st's first scores of unit x
+      auto start = [&](const Unit& x, int st) {
+        const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1], n = st == 0 ? n0 : n1;
+        if (n <= 0) return;
+        const bool with_other = x.shared && (st == 0 ? n1 : n0) > 0;
+        const uint32_t pos = st == 1 && with_other ? kpos : it++;
+        if (st == 0) kpos = pos;
+        wait(&q_full[st], qn[st]++ & 1u);
+        landed(pos);
+        score(st, pos, st == 1 || !with_other, n == 1);
+      };
+      auto unit_of = [&](int un) -> Unit {
         wait(&u_full[un % kUnits], (un / kUnits) & 1u);
-        if (!ok) break;
-        const Unit& x = tb.units[un % kUnits];
+        return ok ? tb.units[un % kUnits] : Unit();
+      };
+      int64_t u = blockIdx.x;
+      Unit x = u < n_units ? unit_of(0) : Unit();
+      if (u < n_units) {
+        start(x, 0);
+        start(x, 1);
+      }
+      for (int un = 0; u < n_units && ok; ++un) {
+        u += gridDim.x;
         const int t0a = x.t0[0], t0b = x.t0[1];
-        const int n0 = x.t1[0] - t0a, n1 = x.t1[1] - t0b;
+        const int n0 = x.t1[0] - t0a, n1 = x.t1[1] - t0b, most = max(n0, n1);
         const bool shared = x.shared;
         auto with_a = [&](int j) { return shared && j < n0; };  // stream b reads stream a's tile j
         auto with_b = [&](int j) { return shared && j < n1; };
@@ -649,23 +613,29 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (!more) umma_commit<false>(smem_u32(&o_done[st]));
           if (more) score(st, pk, k_release, j + 2 == n);
         };
-        if (n0 > 0) {
-          wait(&q_full[0], qn[0]++ & 1u);
-          kpos = it++;
-          landed(kpos);
-          score(0, kpos, !with_b(0), n0 == 1);
+        // Stream a then b of each tile.  At the end the next unit's scores of stream a go before
+        // stream b's last PV unless b takes a tile of its own for it (the ring's order).
+        const bool next = u < n_units;
+        Unit y = x;
+        if (next) y = unit_of(un + 1);
+        bool begun = !next;  // stream a's next scores are issued (or there are none)
+#pragma unroll 1
+        for (int i = 0; i < 2 * most && ok; ++i) {
+          const int st = i & 1, j = i >> 1;
+          if (st == 0) {
+            if (j < n0) step(0, j, t0a + j, n0, true, !with_b(j), true, !with_b(j + 1));
+          } else if (j < n1) {
+            if (j == most - 1 && !begun && with_a(j)) {
+              start(y, 0);
+              begun = true;
+            }
+            step(1, j, t0b + j, n1, !with_a(j), true, !with_a(j + 1), true);
+          }
         }
-        if (n1 > 0) {
-          wait(&q_full[1], qn[1]++ & 1u);
-          const uint32_t pos = with_a(0) ? kpos : it++;
-          landed(pos);
-          score(1, pos, true, n1 == 1);
-        }
-        for (int j = 0; j < max(n0, n1) && ok; ++j) {
-          if (j < n0) step(0, j, t0a + j, n0, true, !with_b(j), true, !with_b(j + 1));
-          if (j < n1) step(1, j, t0b + j, n1, !with_a(j), true, !with_a(j + 1), true);
-        }
+        if (!begun) start(y, 0);
+        if (next) start(y, 1);
         mbar_arrive(smem_u32(&u_empty[un % kUnits]));
+        x = y;
       }
       if (!ok) {
         *abort_flag = 1;
@@ -705,6 +675,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       // page rows that this row sees
       const int seen = BLOCK ? max(0, min(x.lim0 + st * kTok + tk, x.len)) : 0;
       const uint32_t tiles_after = tiles + (BLOCK ? max(x.t1[0], x.t1[1]) : 0);
+      const bool any_row = (r & ~31) / G < x.n_tok[st];  // (else the warp only passes its tiles on)
       float m = -INFINITY;
       float sum = 0.f;
       for (int j = 0; j < n; ++j) {
@@ -713,6 +684,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           break;
         }
         ++sn;
+        if (!any_row) {
+          if (lane < 2) mbar_arrive(smem_u32(&p_ready[2 * st + lane]));
+          continue;
+        }
         tc_fence_after();
         uint32_t sv[4][32];
 #pragma unroll
@@ -721,14 +696,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const bool page = BLOCK && t0 + j >= mt;
         const int valid = page ? seen - (t0 + j - mt) * kTile : M - (t0 + j) * kTile;
         const uint32_t bad = BLOCK ? *const_cast<volatile uint32_t*>(&tb.bad[(tiles + j) % kBadRing]) : 0u;
-        bool plain = valid >= kTile && bad == 0u;
-        if (!__all_sync(0xffffffffu, plain)) {
+        if (!__all_sync(0xffffffffu, valid >= kTile && bad == 0u)) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            // a bit per key that is seen: below the limit, and its page usable
+            const int n_seen = valid - 32 * c;
+            uint32_t keep = n_seen >= 32 ? 0xFFFFFFFFu : n_seen <= 0 ? 0u : (1u << n_seen) - 1u;
+            if (BLOCK) keep &= ~(((bad >> (2 * c)) & 1u) * 0xFFFFu | ((bad >> (2 * c + 1)) & 1u) * 0xFFFF0000u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= valid || (BLOCK && ((bad >> (2 * c + (e >> 4))) & 1u))) sv[c][e] = 0xFF800000u;
-          plain = false;
+            for (int e = 0; e < 32; ++e) sv[c][e] = (keep >> e) & 1u ? sv[c][e] : 0xFF800000u;
+          }
         }
         float mx[4];
 #pragma unroll
@@ -740,8 +717,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           mx[c] = max3(mx[c], __uint_as_float(sv[c][31]), __uint_as_float(sv[c][31]));
         }
         const float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.qscale;  // (qscale > 0; NaN kept)
-        // the polynomial takes finite arguments only
-        plain = plain && top > -INFINITY && top < INFINITY;
         const bool need = top > m + kHeadroom;
         if (__any_sync(0xffffffffu, need)) {
           const float alpha = need ? ex2_ftz(m - top) : 1.f;  // 0 while m is still -inf
@@ -762,33 +737,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const float base = m == -INFINITY ? 0.f : m;
         const f32x2 base2 = pack2(-base, -base);
         f32x2 add[2] = {0ull, 0ull};
-        auto weights = [&](auto mixed) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pw[32];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pw[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const uint32_t s0 = sv[2 * c + (e >> 4)][2 * (e & 15)], s1 = sv[2 * c + (e >> 4)][2 * (e & 15) + 1];
-              const f32x2 v = fma2(pack2(__uint_as_float(s0), __uint_as_float(s1)), scale2, base2);
-              float p0, p1;
-              if (decltype(mixed)::value && (e & 3) < kPolyOf8 / 2) {
-                ex2_poly(v, p0, p1);
-              } else {
-                unpack2(v, p0, p1);
-                p0 = ex2_ftz(p0);
-                p1 = ex2_ftz(p1);
-              }
-              add[e & 1] = add2(add[e & 1], pack2(p0, p1));
-              pw[e] = msa::float2_to_bf16x2(p0, p1);
-            }
-            tmem_st32(s_col + 32 * c, pw);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * st + c]));
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t s0 = sv[2 * c + (e >> 4)][2 * (e & 15)], s1 = sv[2 * c + (e >> 4)][2 * (e & 15) + 1];
+            float p0, p1;
+            unpack2(fma2(pack2(__uint_as_float(s0), __uint_as_float(s1)), scale2, base2), p0, p1);
+            p0 = ex2_ftz(p0);
+            p1 = ex2_ftz(p1);
+            add[e & 1] = add2(add[e & 1], pack2(p0, p1));
+            pw[e] = msa::float2_to_bf16x2(p0, p1);
           }
-        };
-        if (__all_sync(0xffffffffu, plain)) weights(Yes{}); else weights(No{});
+          tmem_st32(s_col + 32 * c, pw);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&p_ready[2 * st + c]));
+        }
         float s0, s1;
         unpack2(add2(add[0], add[1]), s0, s1);
         sum += s0 + s1;
@@ -811,12 +778,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (n > 0) {
           tmem_ld32(o_col + 32 * c, o);
           tmem_wait_ld();
-        }
-        if (BLOCK && !(n > 0)) {
+        } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (mine && poisoned) add_not_finite(a, x, seen, 32 * c, o);
         if (mine && BLOCK) {
           __nv_bfloat16* dst = a.out + row * kD + 32 * c;
 #pragma unroll
@@ -832,6 +797,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           for (int e = 0; e < 4; ++e) st_global_v8(part + row * kD + 32 * c + 8 * e, *reinterpret_cast<uint32_t(*)[8]>(&o[8 * e]));
         }
       }
+      if (BLOCK && mine && poisoned) add_not_finite(a, x, seen, a.out + row * kD);
       tc_fence_before();  // (O is read: the next unit's first PV may overwrite it)
       if (!BLOCK && mine) stat[row] = make_float2(m, sum);  // (no tiles: -inf and 0)
       __syncwarp();
@@ -847,20 +813,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     // again before), so that the phases it waits for are never ambiguous.
     bool ok = true;
     uint32_t it = 0, prep = 0;
-    auto pass = [&](int tiles, auto prepare) {
-      for (int i = 0; i < tiles && ok; ++i, ++it) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[it % kSlots]), (it / kSlots) & 1u, abort_flag))) {
-          ok = false;
-          return;
-        }
-        prepare(sbase + kOffRing + (it % kSlots) * kSlotBytes);
-        if (lane == 0) mbar_arrive(smem_u32(&empty[it % kSlots]));
-        __syncwarp();
-      }
-    };
-    auto keys = [&](bool any) { pass(any, [](uint32_t) {}); };
-    auto prepare_values = [&](const Unit& x, int tile, uint32_t vt, int un) {
-      if (!prepared(x, tile)) return;
+    auto prepare = [&](const Unit& x, int tile, uint32_t vt, int un) {
       const int valid = valid_keys(x, tile), rows = (valid + 15) & ~15;
       for (int i = lane; i < (rows - valid) * 16; i += 32) {
         const int row = valid + (i >> 4), c16 = i & 15;
@@ -907,6 +860,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (lane == 0) mbar_arrive(smem_u32(&v_ready[prep % kSlots]));
       ++prep;
     };
+    auto pass = [&](const Unit& x, int tile, bool is_v, int un) {
+      if (!ok) return;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[it % kSlots]), (it / kSlots) & 1u, abort_flag))) {
+        ok = false;
+        return;
+      }
+      if (is_v && prepared(x, tile)) prepare(x, tile, sbase + kOffRing + (it % kSlots) * kSlotBytes, un);
+      if (lane == 0) mbar_arrive(smem_u32(&empty[it % kSlots]));
+      __syncwarp();
+      ++it;
+    };
     int un = 0;
     for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
       if (!__all_sync(0xffffffffu, unit_wait(un))) {
@@ -916,14 +880,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       const Unit& x = tb.units[un % kUnits];
       const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
       auto own_b = [&](int j) { return j < n1 && (!x.shared || j >= n0); };
-      // (the order of the loads: first key tiles, then value tile j and key tile j + 1 by stream)
-      keys(n0 > 0);
-      keys(own_b(0));
-      for (int j = 0; j < max(n0, n1) && ok; ++j) {
-        pass(j < n0, [&](uint32_t vt) { prepare_values(x, x.t0[0] + j, vt, un); });
-        keys(j + 1 < n0);
-        pass(own_b(j), [&](uint32_t vt) { prepare_values(x, x.t0[1] + j, vt, un); });
-        keys(own_b(j + 1));
+#pragma unroll 1
+      for (int i = -2; i < 2 * max(n0, n1) && ok; ++i) {  // (the order of the loads)
+        const int st = i & 1, j = i >> 1;
+        auto own = [&](int k) { return st == 0 ? k < n0 : own_b(k); };
+#pragma unroll 1
+        for (int v = 1; v >= 0; --v) {
+          const int k = v ? j : j + 1;
+          if (k >= 0 && own(k)) pass(x, x.t0[st] + k, v != 0, un);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&u_empty[un % kUnits]));
@@ -934,21 +899,54 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    // ---- units
-    if (lane == 0) {
-      int un = 0;
-      for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++un) {
-        const Unit x = unit_at(u);
-        if (!mbar_wait(smem_u32(&u_empty[un % kUnits]), ((un / kUnits) & 1u) ^ 1u, abort_flag)) {
-          *abort_flag = 1;
-          msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
-          break;
-        }
-        tb.units[un % kUnits] = x;
-        mbar_arrive(smem_u32(&u_full[un % kUnits]));
+    // ---- units, each worked out before the queries of the one before it are loaded
+    if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+    bool ok = true;
+    uint32_t qn[2] = {0, 0};  // query tiles loaded per stream
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
+      return ok;
+    };
+    auto load_q = [&](const Unit& x, int st) {
+      if (!ok || x.t1[st] <= x.t0[st]) return;
+      if (!wait(&q_empty[st], (qn[st] & 1u) ^ 1u)) return;
+      ++qn[st];
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&q_full[st]);
+        const uint32_t dst = sbase + kOffQ + st * kSlotBytes;
+        mbar_arrive_expect_tx(bar, kSlotBytes);
+        tma_load_4d(dst, &tm_q, bar, 0, x.h * G, x.tok[st], x.l);
+        tma_load_4d(dst + kHalfBytes, &tm_q, bar, kHalf, x.h * G, x.tok[st], x.l);
       }
+      __syncwarp();
+    };
+    int64_t u = blockIdx.x;
+    for (int un = 0; ok; u += gridDim.x, ++un) {
+      if (u < n_units) {
+        const Unit x = unit_at(u);
+        if (!wait(&u_empty[un % kUnits], ((un / kUnits) & 1u) ^ 1u)) break;
+        if (lane == 0) {
+          tb.units[un % kUnits] = x;
+          mbar_arrive(smem_u32(&u_full[un % kUnits]));
+        }
+        __syncwarp();
+      }
+      if (un > 0) {  // (its place is not taken again before this warp has come by)
+        const Unit& x = tb.units[(un - 1) % kUnits];
+        load_q(x, 0);
+        load_q(x, 1);
+      }
+      if (u >= n_units) break;
     }
-    __syncwarp();
+    if (!ok) {
+      if (lane == 0) {
+        *abort_flag = 1;
+        msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
+        for (int st = 0; st < 2; ++st)
+          if (qn[st] > 0) mbar_drain(smem_u32(&q_full[st]), (qn[st] - 1) & 1u);
+      }
+      __syncwarp();
+    }
   }
 
   tc_fence_before();
