@@ -121,6 +121,14 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       : "memory");
 }
 
+// Bounded wait whose polling loop is one copy for all roles (instruction fetch).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return tc::mbar_wait(bar, parity, abort_flag);
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag);
+}
+
 // 4D tiled TMA load (no multicast): [128 / G tokens][G heads][64 dims] of one layer's queries.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             int w) {
@@ -399,7 +407,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     return (valid_keys(x, tile) & 15) != 0 || (BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0);
   };
   // unit un of this CTA (every lane of the caller's warp, or its one thread, waits)
-  auto unit_wait = [&](int un) -> bool { return mbar_wait(smem_u32(&u_full[un % kUnits]), (un / kUnits) & 1u, abort_flag); };
+  auto unit_wait = [&](int un) -> bool { return wait_for(smem_u32(&u_full[un % kUnits]), (un / kUnits) & 1u, abort_flag); };
 
   // (setmaxnreg in each role's own branch: the compiler allocates what follows by it)
   if (warp == kTmaWarp) {
@@ -413,7 +421,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint32_t it = 0;                // ring position
     uint32_t tiles = 0;             // key tiles of the block form so far
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
+      if (!__all_sync(0xffffffffu, wait_for(smem_u32(bar), parity, abort_flag))) ok = false;
       return ok;
     };
     // page ids of 512 consecutive rows of a sequence, a lane per 16 rows
@@ -522,24 +530,25 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       bool ok = true, issued = false;
       uint32_t it = 0;               // ring position of the next tile
       uint32_t prep = 0;             // tiles that warp 10 prepared
-      uint32_t qn[2] = {0, 0};       // query tiles used per stream
-      uint32_t pn[2] = {0, 0};       // weight tiles used per stream
+      uint32_t qn = 0, pn = 0;       // parities of the query and weight tiles used, a bit per stream
       uint32_t kpos = 0, vpos = 0;   // (shared) ring positions of stream a's current K and V
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && mbar_wait(smem_u32(bar), parity, abort_flag);
+        ok = ok && wait_for(smem_u32(bar), parity, abort_flag);
       };
       auto landed = [&](uint32_t pos) { wait(&full[pos % kSlots], (pos / kSlots) & 1u); };
       // scores of stream st over the key tile in ring position `pos` (landed); `release`: the
       // tile's last use; `last`: the queries' last use
       auto score = [&](int st, uint32_t pos, bool release, bool last) {
         if (!ok) return;
-        const uint64_t kt = at(rows_desc, kOffRing + (pos % kSlots) * kSlotBytes);
-        const uint64_t qt = at(rows_desc, kOffQ + st * kSlotBytes);
+        uint64_t kt = at(rows_desc, kOffRing + (pos % kSlots) * kSlotBytes);
+        uint64_t qt = at(rows_desc, kOffQ + st * kSlotBytes);
         const uint32_t d = tmem_base + kColS + (uint32_t)(st * kTile);
-#pragma unroll
+#pragma unroll 1
         for (int ks = 0; ks < kD / 16; ++ks) {
-          const uint32_t off = (uint32_t)((ks >> 2) * kHalfBytes + (ks & 3) * 32);
-          umma<false, false>(d, at(qt, off), at(kt, off), idesc_s, ks > 0 ? 1u : 0u);
+          umma<false, false>(d, qt, kt, idesc_s, ks > 0 ? 1u : 0u);
+          const uint64_t on = ks == 3 ? (kHalfBytes - 96) >> 4 : 2;  // 32 bytes on, or to the other half
+          qt += on;
+          kt += on;
         }
         umma_commit<false>(smem_u32(&s_ready[st]));
         if (release) umma_commit<false>(smem_u32(&empty[pos % kSlots]));
@@ -549,16 +558,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       // O += P V of stream st over the value tile in ring position `pos` (ready): 16-key steps
       // 4 h .. 4 h + 3 as far as there are keys
       auto weigh = [&](int st, uint32_t pos, int h, int n_ks, bool first) {
-        wait(&p_ready[2 * st + h], pn[st] & 1u);
+        wait(&p_ready[2 * st + h], (pn >> st) & 1u);
         if (!ok) return;
         tc_fence_after();
         const uint64_t vt = at(cols_desc, kOffRing + (pos % kSlots) * kSlotBytes + h * 4 * 2048);
         const uint32_t p = tmem_base + kColS + (uint32_t)(st * kTile + h * 32);
         const uint32_t d = tmem_base + kColO + (uint32_t)(st * kTile);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          if (4 * h + ks < n_ks)
-            umma_ts(d, p + (uint32_t)(8 * ks), at(vt, ks * 2048), idesc_pv, (!first || 4 * h + ks > 0) ? 1u : 0u);
+#pragma unroll 1
+        for (int ks = 0; ks < min(4, n_ks - 4 * h); ++ks)
+          umma_ts(d, p + (uint32_t)(8 * ks), at(vt, ks * 2048), idesc_pv, (!first || 4 * h + ks > 0) ? 1u : 0u);
       };
       // stream st's first scores of unit x
       auto start = [&](const Unit& x, int st) {
@@ -567,7 +575,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const bool with_other = x.shared && (st == 0 ? n1 : n0) > 0;
         const uint32_t pos = st == 1 && with_other ? kpos : it++;
         if (st == 0) kpos = pos;
-        wait(&q_full[st], qn[st]++ & 1u);
+        wait(&q_full[st], (qn >> st) & 1u);
+        qn ^= 1u << st;
         landed(pos);
         score(st, pos, st == 1 || !with_other, n == 1);
       };
@@ -577,24 +586,35 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       };
       int64_t u = blockIdx.x;
       Unit x = u < n_units ? unit_of(0) : Unit();
-      if (u < n_units) {
-        start(x, 0);
-        start(x, 1);
-      }
+#pragma unroll 1
+      for (int st = 0; st < 2 && u < n_units; ++st) start(x, st);
       for (int un = 0; u < n_units && ok; ++un) {
         u += gridDim.x;
-        const int t0a = x.t0[0], t0b = x.t0[1];
-        const int n0 = x.t1[0] - t0a, n1 = x.t1[1] - t0b, most = max(n0, n1);
+        const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1], most = max(n0, n1);
         const bool shared = x.shared;
-        auto with_a = [&](int j) { return shared && j < n0; };  // stream b reads stream a's tile j
-        auto with_b = [&](int j) { return shared && j < n1; };
-        // PV of tile j of stream st, then the scores of its tile j + 1
-        auto step = [&](int st, int j, int tile, int n, bool own, bool v_release, bool k_own, bool k_release) {
+        const bool next = u < n_units;
+        Unit y = x;
+        if (next) y = unit_of(un + 1);
+        bool begun = !next;  // stream a's next scores are issued (or there are none)
+        // Per tile stream a, then b: the PV, then the scores of the stream's next tile.  At the
+        // end the next unit's scores of stream a go before stream b's last PV unless b takes a
+        // tile of its own for it (the ring's order).
+#pragma unroll 1
+        for (int i = 0; i < 2 * most && ok; ++i) {
+          const int st = i & 1, j = i >> 1;
+          const int n = st ? n1 : n0, n_other = st ? n0 : n1;
+          if (j >= n) continue;
+          const bool with = shared && j < n_other, with_next = shared && j + 1 < n_other;  // both use the tile
+          if (st == 1 && with && !begun && j == most - 1) {
+            start(y, 0);
+            begun = true;
+          }
+          const bool own = st == 0 || !with, more = j + 1 < n;
+          const int tile = (st ? x.t0[1] : x.t0[0]) + j;
           const uint32_t pv = own ? it++ : vpos;
-          if (st == 0) vpos = pv;
-          const bool more = j + 1 < n;
+          vpos = pv;
           uint32_t pk = kpos;
-          if (more && k_own) pk = it++;
+          if (more && (st == 0 || !with_next)) pk = it++;
           if (st == 0) kpos = pk;
           const int n_ks = (valid_keys(x, tile) + 15) >> 4;
           if (own) {
@@ -604,36 +624,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
               ++prep;
             }
           }
-          weigh(st, pv, 0, n_ks, j == 0);
           if (more) landed(pk);
-          weigh(st, pv, 1, n_ks, j == 0);
-          ++pn[st];
-          if (!ok) return;
-          if (v_release) umma_commit<false>(smem_u32(&empty[pv % kSlots]));
-          if (!more) umma_commit<false>(smem_u32(&o_done[st]));
-          if (more) score(st, pk, k_release, j + 2 == n);
-        };
-        // Stream a then b of each tile.  At the end the next unit's scores of stream a go before
-        // stream b's last PV unless b takes a tile of its own for it (the ring's order).
-        const bool next = u < n_units;
-        Unit y = x;
-        if (next) y = unit_of(un + 1);
-        bool begun = !next;  // stream a's next scores are issued (or there are none)
 #pragma unroll 1
-        for (int i = 0; i < 2 * most && ok; ++i) {
-          const int st = i & 1, j = i >> 1;
-          if (st == 0) {
-            if (j < n0) step(0, j, t0a + j, n0, true, !with_b(j), true, !with_b(j + 1));
-          } else if (j < n1) {
-            if (j == most - 1 && !begun && with_a(j)) {
-              start(y, 0);
-              begun = true;
-            }
-            step(1, j, t0b + j, n1, !with_a(j), true, !with_a(j + 1), true);
+          for (int h = 0; h < 2; ++h) weigh(st, pv, h, n_ks, j == 0);
+          pn ^= 1u << st;
+          if (!ok) break;
+          if (st == 1 || !with) umma_commit<false>(smem_u32(&empty[pv % kSlots]));
+          if (more) {
+            score(st, pk, st == 1 || !with_next, j + 2 == n);
+          } else {
+            umma_commit<false>(smem_u32(&o_done[st]));
           }
         }
-        if (!begun) start(y, 0);
-        if (next) start(y, 1);
+#pragma unroll 1
+        for (int st = begun ? 1 : 0; st < 2 && next; ++st) start(y, st);
         mbar_arrive(smem_u32(&u_empty[un % kUnits]));
         x = y;
       }
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       float m = -INFINITY;
       float sum = 0.f;
       for (int j = 0; j < n; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[st]), sn & 1u, abort_flag))) {
+        if (!__all_sync(0xffffffffu, wait_for(smem_u32(&s_ready[st]), sn & 1u, abort_flag))) {
           ok = false;
           break;
         }
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (!ok) break;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no key seen: output 0; a NaN sum is kept)
       if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[st]), on & 1u, abort_flag))) {
+        if (!__all_sync(0xffffffffu, wait_for(smem_u32(&o_done[st]), on & 1u, abort_flag))) {
           ok = false;
           break;
         }
@@ -862,7 +866,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     };
     auto pass = [&](const Unit& x, int tile, bool is_v, int un) {
       if (!ok) return;
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[it % kSlots]), (it / kSlots) & 1u, abort_flag))) {
+      if (!__all_sync(0xffffffffu, wait_for(smem_u32(&full[it % kSlots]), (it / kSlots) & 1u, abort_flag))) {
         ok = false;
         return;
       }
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     bool ok = true;
     uint32_t qn[2] = {0, 0};  // query tiles loaded per stream
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
+      if (!__all_sync(0xffffffffu, wait_for(smem_u32(bar), parity, abort_flag))) ok = false;
       return ok;
     };
     auto load_q = [&](const Unit& x, int st) {
