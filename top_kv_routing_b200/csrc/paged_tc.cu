@@ -22,12 +22,14 @@
 //                        memory, M = N = 128), O += P V (weights from tensor memory, written
 //                        over their scores; V read MN-major from its rows).  PV_a(j), S_a(j+1),
 //                        PV_b(j), S_b(j+1), ...: while one stream's softmax runs, the tensor
-//                        cores work for the other; the next unit's first scores go
-//                        before stream b's last PV.  A PV starts on the weights of the first 64
-//                        keys while the softmax computes those of the others;
-//   warp 10              prepares value tiles before their PV: rows past the last valid one,
-//                        which may hold anything, are zeroed, and values that are not finite
-//                        taken out where some rows must not see them;
+//                        cores work for the other.  A PV starts on the weights of the first 64
+//                        keys while the softmax computes those of the others.  Each pair of PV
+//                        and S is one command word, so that little but the MMAs themselves is
+//                        left to the thread (working them out itself took it as long again);
+//   warp 10              writes the commands as the tiles land, and prepares value tiles before
+//                        their PV: rows past the last valid one, which may hold anything, are
+//                        zeroed, and values that are not finite taken out where some rows must
+//                        not see them;
 //   warp 11              works out the units ahead of everyone else (a ring of kUnits), and loads
 //                        their query rows (4D boxes);
 //   warps 0..3, 4..7     the softmax of stream a and of stream b: a thread per row, with the
@@ -60,6 +62,7 @@ constexpr int kHalf = 64;                 // dims of a 128-byte swizzled row
 constexpr int kHalfBytes = kTile * 128;   // 16 KB: 128 rows x 64 dims
 constexpr int kSlotBytes = 2 * kHalfBytes;  // one K or V tile, or one query tile
 constexpr int kSlots = 5;
+constexpr int kCommands = 16;             // (10 at most wait: two a tile of the ring)
 constexpr int kUnits = 4;                 // units worked out ahead
 constexpr int kWarpsTc = 12;              // 0..7 softmax, 8 MMA, 9 TMA, 10 value tiles, 11 units
 constexpr int kThreadsTc = kWarpsTc * 32;
@@ -97,8 +100,24 @@ struct TablesTc {
   int splits;
   uint32_t tmem;
   int abort;
+  uint32_t commands[kCommands];
   Unit units[kUnits];      // unit u of this CTA in place u % kUnits
   uint32_t bad[kBadRing];  // block form: per tile, its 16-row pieces without a usable page
+};
+
+// A command of the MMA thread: for stream `kStreamB`, O += P V over a value tile and then the
+// scores over a key tile (either may be missing).
+enum : uint32_t {
+  kStreamB = 1u,
+  kWeigh = 2u,        // PV: 16-key steps in bits 12..15, ring slot in bits 16..18
+  kFirst = 4u,        // the unit's first PV of the stream (O starts from it)
+  kFreeV = 8u,        // the tile's last use
+  kOutput = 16u,      // O is complete
+  kScore = 32u,       // scores: ring slot in bits 20..22
+  kAwaitQ = 64u,      // the unit's first scores of the stream: its queries have to land
+  kFreeK = 128u,      // the tile's last use
+  kFreeQ = 256u,      // the queries' last use
+  kEnd = 512u,
 };
 
 constexpr int kOffQ = 0;
@@ -119,14 +138,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-
-// Bounded wait whose polling loop is one copy for all roles (instruction fetch).
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return tc::mbar_wait(bar, parity, abort_flag);
-}
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, abort_flag);
 }
 
 // 4D tiled TMA load (no multicast): [128 / G tokens][G heads][64 dims] of one layer's queries.
@@ -210,9 +221,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   uint64_t* s_ready = q_empty + 2;       // [2] scores in tensor memory (and the stream's PV before them done)
   uint64_t* p_ready = s_ready + 2;       // [2][2] weights of keys 0..63, 64..127 in tensor memory (4 warps)
   uint64_t* o_done = p_ready + 4;        // [2] the stream's last PV of the unit done
-  uint64_t* v_ready = o_done + 2;        // [kSlots] the n-th tile that warp 10 prepares (n % kSlots)
-  uint64_t* u_full = v_ready + kSlots;   // [kUnits] unit worked out
-  uint64_t* u_empty = u_full + kUnits;   // [kUnits] not needed any more (TMA, MMA, value, 8 softmax warps)
+  uint64_t* c_full = o_done + 2;         // [kCommands] command written
+  uint64_t* u_full = c_full + kCommands; // [kUnits] unit worked out
+  uint64_t* u_empty = u_full + kUnits;   // [kUnits] not needed any more (TMA, commands, 8 softmax warps)
   uint64_t* drain = u_empty + kUnits;
   volatile int* abort_flag = &tb.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,11 +234,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 2);
-      mbar_init(smem_u32(&v_ready[s]), 1);
     }
+    for (int s = 0; s < kCommands; ++s) mbar_init(smem_u32(&c_full[s]), 1);
     for (int s = 0; s < kUnits; ++s) {
       mbar_init(smem_u32(&u_full[s]), 1);
-      mbar_init(smem_u32(&u_empty[s]), 11);
+      mbar_init(smem_u32(&u_empty[s]), 10);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&q_full[x]), 1);
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     return (valid_keys(x, tile) & 15) != 0 || (BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0);
   };
   // unit un of this CTA (every lane of the caller's warp, or its one thread, waits)
-  auto unit_wait = [&](int un) -> bool { return wait_for(smem_u32(&u_full[un % kUnits]), (un / kUnits) & 1u, abort_flag); };
+  auto unit_wait = [&](int un) -> bool { return mbar_wait(smem_u32(&u_full[un % kUnits]), (un / kUnits) & 1u, abort_flag); };
 
   // (setmaxnreg in each role's own branch: the compiler allocates what follows by it)
   if (warp == kTmaWarp) {
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint32_t it = 0;                // ring position
     uint32_t tiles = 0;             // key tiles of the block form so far
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (!__all_sync(0xffffffffu, wait_for(smem_u32(bar), parity, abort_flag))) ok = false;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
       return ok;
     };
     // page ids of 512 consecutive rows of a sequence, a lane per 16 rows
@@ -525,121 +536,58 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       // leading offset), the high words are the same for all tiles of a kind.
       constexpr uint32_t idesc_s = idesc_make(kRows, kTile, false);
       constexpr uint32_t idesc_pv = idesc_make_bmn(kRows, kD);
-      const uint64_t rows_desc = sw128_desc(sbase), cols_desc = sw128_desc_mn(sbase, kHalfBytes, 1024);
-      auto at = [](uint64_t desc, uint32_t bytes) -> uint64_t { return desc + (uint64_t)(bytes >> 4); };
+      const uint64_t rows_desc = sw128_desc(sbase + kOffRing), q_desc = sw128_desc(sbase + kOffQ);
+      const uint64_t cols_desc = sw128_desc_mn(sbase + kOffRing, kHalfBytes, 1024);
       bool ok = true, issued = false;
-      uint32_t it = 0;               // ring position of the next tile
-      uint32_t prep = 0;             // tiles that warp 10 prepared
       uint32_t qn = 0, pn = 0;       // parities of the query and weight tiles used, a bit per stream
-      uint32_t kpos = 0, vpos = 0;   // (shared) ring positions of stream a's current K and V
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && wait_for(smem_u32(bar), parity, abort_flag);
+        ok = ok && mbar_wait(smem_u32(bar), parity & 1u, abort_flag);
       };
-      auto landed = [&](uint32_t pos) { wait(&full[pos % kSlots], (pos / kSlots) & 1u); };
-      // scores of stream st over the key tile in ring position `pos` (landed); `release`: the
-      // tile's last use; `last`: the queries' last use
-      auto score = [&](int st, uint32_t pos, bool release, bool last) {
-        if (!ok) return;
-        uint64_t kt = at(rows_desc, kOffRing + (pos % kSlots) * kSlotBytes);
-        uint64_t qt = at(rows_desc, kOffQ + st * kSlotBytes);
-        const uint32_t d = tmem_base + kColS + (uint32_t)(st * kTile);
 #pragma unroll 1
-        for (int ks = 0; ks < kD / 16; ++ks) {
-          umma<false, false>(d, qt, kt, idesc_s, ks > 0 ? 1u : 0u);
-          const uint64_t on = ks == 3 ? (kHalfBytes - 96) >> 4 : 2;  // 32 bytes on, or to the other half
-          qt += on;
-          kt += on;
-        }
-        umma_commit<false>(smem_u32(&s_ready[st]));
-        if (release) umma_commit<false>(smem_u32(&empty[pos % kSlots]));
-        if (last) umma_commit<false>(smem_u32(&q_empty[st]));
-        issued = true;
-      };
-      // O += P V of stream st over the value tile in ring position `pos` (ready): 16-key steps
-      // 4 h .. 4 h + 3 as far as there are keys
-      auto weigh = [&](int st, uint32_t pos, int h, int n_ks, bool first) {
-        wait(&p_ready[2 * st + h], (pn >> st) & 1u);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t vt = at(cols_desc, kOffRing + (pos % kSlots) * kSlotBytes + h * 4 * 2048);
-        const uint32_t p = tmem_base + kColS + (uint32_t)(st * kTile + h * 32);
-        const uint32_t d = tmem_base + kColO + (uint32_t)(st * kTile);
-#pragma unroll 1
-        for (int ks = 0; ks < min(4, n_ks - 4 * h); ++ks)
-          umma_ts(d, p + (uint32_t)(8 * ks), at(vt, ks * 2048), idesc_pv, (!first || 4 * h + ks > 0) ? 1u : 0u);
-      };
-      // stream st's first scores of unit x
-      auto start = [&](const Unit& x, int st) {
-        const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1], n = st == 0 ? n0 : n1;
-        if (n <= 0) return;
-        const bool with_other = x.shared && (st == 0 ? n1 : n0) > 0;
-        const uint32_t pos = st == 1 && with_other ? kpos : it++;
-        if (st == 0) kpos = pos;
-        wait(&q_full[st], (qn >> st) & 1u);
-        qn ^= 1u << st;
-        landed(pos);
-        score(st, pos, st == 1 || !with_other, n == 1);
-      };
-      auto unit_of = [&](int un) -> Unit {
-        wait(&u_full[un % kUnits], (un / kUnits) & 1u);
-        return ok ? tb.units[un % kUnits] : Unit();
-      };
-      int64_t u = blockIdx.x;
-      Unit x = u < n_units ? unit_of(0) : Unit();
-#pragma unroll 1
-      for (int st = 0; st < 2 && u < n_units; ++st) start(x, st);
-      for (int un = 0; u < n_units && ok; ++un) {
-        u += gridDim.x;
-        const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1], most = max(n0, n1);
-        const bool shared = x.shared;
-        const bool next = u < n_units;
-        Unit y = x;
-        if (next) y = unit_of(un + 1);
-        bool begun = !next;  // stream a's next scores are issued (or there are none)
-        // Per tile stream a, then b: the PV, then the scores of the stream's next tile.  At the
-        // end the next unit's scores of stream a go before stream b's last PV unless b takes a
-        // tile of its own for it (the ring's order).
-#pragma unroll 1
-        for (int i = 0; i < 2 * most && ok; ++i) {
-          const int st = i & 1, j = i >> 1;
-          const int n = st ? n1 : n0, n_other = st ? n0 : n1;
-          if (j >= n) continue;
-          const bool with = shared && j < n_other, with_next = shared && j + 1 < n_other;  // both use the tile
-          if (st == 1 && with && !begun && j == most - 1) {
-            start(y, 0);
-            begun = true;
+      for (uint32_t i = 0;; ++i) {
+        wait(&c_full[i % kCommands], i / kCommands);
+        if (!ok) break;
+        const uint32_t w = *const_cast<volatile uint32_t*>(&tb.commands[i % kCommands]);
+        if (w & kEnd) break;
+        const uint32_t st = w & kStreamB;
+        const uint32_t s_cols = tmem_base + kColS + st * kTile;
+        if (w & kWeigh) {
+          const int n_ks = (w >> 12) & 15;
+          const uint32_t slot = (w >> 16) & 7u, o_cols = tmem_base + kColO + st * kTile;
+          const uint64_t vt = cols_desc + (uint64_t)(slot * (kSlotBytes >> 4));
+          const uint32_t acc = w & kFirst ? 0u : 1u;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            wait(&p_ready[2 * st + h], pn >> st);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+              if (ks < n_ks) umma_ts(o_cols, s_cols + 8 * ks, vt + ks * (2048 >> 4), idesc_pv, ks > 0 ? 1u : acc);
           }
-          const bool own = st == 0 || !with, more = j + 1 < n;
-          const int tile = (st ? x.t0[1] : x.t0[0]) + j;
-          const uint32_t pv = own ? it++ : vpos;
-          vpos = pv;
-          uint32_t pk = kpos;
-          if (more && (st == 0 || !with_next)) pk = it++;
-          if (st == 0) kpos = pk;
-          const int n_ks = (valid_keys(x, tile) + 15) >> 4;
-          if (own) {
-            landed(pv);
-            if (prepared(x, tile)) {
-              wait(&v_ready[prep % kSlots], (prep / kSlots) & 1u);
-              ++prep;
-            }
-          }
-          if (more) landed(pk);
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) weigh(st, pv, h, n_ks, j == 0);
-          pn ^= 1u << st;
           if (!ok) break;
-          if (st == 1 || !with) umma_commit<false>(smem_u32(&empty[pv % kSlots]));
-          if (more) {
-            score(st, pk, st == 1 || !with_next, j + 2 == n);
-          } else {
-            umma_commit<false>(smem_u32(&o_done[st]));
-          }
+          pn ^= 1u << st;
+          if (w & kOutput) umma_commit<false>(smem_u32(&o_done[st]));
+          if (w & kFreeV) umma_commit<false>(smem_u32(&empty[slot]));
         }
-#pragma unroll 1
-        for (int st = begun ? 1 : 0; st < 2 && next; ++st) start(y, st);
-        mbar_arrive(smem_u32(&u_empty[un % kUnits]));
-        x = y;
+        if (w & kScore) {
+          if (w & kAwaitQ) {
+            wait(&q_full[st], qn >> st);
+            if (!ok) break;
+            qn ^= 1u << st;
+          }
+          const uint32_t slot = (w >> 20) & 7u;
+          const uint64_t kt = rows_desc + (uint64_t)(slot * (kSlotBytes >> 4)), qt = q_desc + (uint64_t)(st * (kSlotBytes >> 4));
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint64_t on = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
+            umma<false, false>(s_cols, qt + on, kt + on, idesc_s, ks > 0 ? 1u : 0u);
+          }
+          umma_commit<false>(smem_u32(&s_ready[st]));
+          if (w & kFreeK) umma_commit<false>(smem_u32(&empty[slot]));
+          if (w & kFreeQ) umma_commit<false>(smem_u32(&q_empty[st]));
+          issued = true;
+        }
       }
       if (!ok) {
         *abort_flag = 1;
@@ -683,7 +631,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       float m = -INFINITY;
       float sum = 0.f;
       for (int j = 0; j < n; ++j) {
-        if (!__all_sync(0xffffffffu, wait_for(smem_u32(&s_ready[st]), sn & 1u, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[st]), sn & 1u, abort_flag))) {
           ok = false;
           break;
         }
@@ -768,7 +716,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (!ok) break;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no key seen: output 0; a NaN sum is kept)
       if (n > 0) {
-        if (!__all_sync(0xffffffffu, wait_for(smem_u32(&o_done[st]), on & 1u, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[st]), on & 1u, abort_flag))) {
           ok = false;
           break;
         }
@@ -813,10 +761,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
   } else if (warp == kValueWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
-    // ---- value tiles.  The warp passes every tile of the ring in order (and no slot is filled
+    // ---- commands and value tiles.  The warp passes every tile of the ring in order (and no slot is filled
     // again before), so that the phases it waits for are never ambiguous.
     bool ok = true;
-    uint32_t it = 0, prep = 0;
+    uint32_t it = 0, cn = 0;  // ring position, commands so far
     auto prepare = [&](const Unit& x, int tile, uint32_t vt, int un) {
       const int valid = valid_keys(x, tile), rows = (valid + 15) & ~15;
       for (int i = lane; i < (rows - valid) * 16; i += 32) {
@@ -861,12 +809,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       __threadfence_block();
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&v_ready[prep % kSlots]));
-      ++prep;
+    };
+    auto command = [&](uint32_t w) {
+      if (!ok) return;
+      if (lane == 0) {
+        *const_cast<volatile uint32_t*>(&tb.commands[cn % kCommands]) = w;
+        mbar_arrive(smem_u32(&c_full[cn % kCommands]));
+      }
+      ++cn;
     };
     auto pass = [&](const Unit& x, int tile, bool is_v, int un) {
       if (!ok) return;
-      if (!__all_sync(0xffffffffu, wait_for(smem_u32(&full[it % kSlots]), (it / kSlots) & 1u, abort_flag))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&full[it % kSlots]), (it / kSlots) & 1u, abort_flag))) {
         ok = false;
         return;
       }
@@ -883,20 +837,38 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       const Unit& x = tb.units[un % kUnits];
       const int n0 = x.t1[0] - x.t0[0], n1 = x.t1[1] - x.t0[1];
-      auto own_b = [&](int j) { return j < n1 && (!x.shared || j >= n0); };
+      const bool shared = x.shared;
+      uint32_t ka = 0, va = 0;  // slots of stream a's key and value tile
 #pragma unroll 1
       for (int i = -2; i < 2 * max(n0, n1) && ok; ++i) {  // (the order of the loads)
         const int st = i & 1, j = i >> 1;
-        auto own = [&](int k) { return st == 0 ? k < n0 : own_b(k); };
+        const int n = st ? n1 : n0, n_other = st ? n0 : n1;
+        if (j >= n) continue;
+        uint32_t w = (uint32_t)st;
 #pragma unroll 1
-        for (int v = 1; v >= 0; --v) {
+        for (int v = 1; v >= 0; --v) {  // value tile j, key tile j + 1
           const int k = v ? j : j + 1;
-          if (k >= 0 && own(k)) pass(x, x.t0[st] + k, v != 0, un);
+          if (k < 0 || k >= n) continue;
+          const bool with = shared && k < n_other;  // both streams use the tile
+          uint32_t slot = v ? va : ka;
+          if (st == 0 || !with) {
+            slot = it % kSlots;
+            pass(x, x.t0[st] + k, v != 0, un);
+          }
+          if (st == 0) (v ? va : ka) = slot;
+          const bool last_use = st == 1 || !with;
+          if (v)
+            w |= kWeigh | (k == 0 ? kFirst : 0u) | (k + 1 == n ? kOutput : 0u) | (last_use ? kFreeV : 0u) |
+                 (uint32_t)((valid_keys(x, x.t0[st] + k) + 15) >> 4) << 12 | slot << 16;
+          else
+            w |= kScore | (k == 0 ? kAwaitQ : 0u) | (k + 1 == n ? kFreeQ : 0u) | (last_use ? kFreeK : 0u) | slot << 20;
         }
+        if (w & (kWeigh | kScore)) command(w);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&u_empty[un % kUnits]));
     }
+    command(kEnd);
     if (!ok && lane == 0) {
       *abort_flag = 1;
       msa::set_err(a.dev_err, MSA_DEVERR_TIMEOUT);
@@ -908,7 +880,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     bool ok = true;
     uint32_t qn[2] = {0, 0};  // query tiles loaded per stream
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (!__all_sync(0xffffffffu, wait_for(smem_u32(bar), parity, abort_flag))) ok = false;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
       return ok;
     };
     auto load_q = [&](const Unit& x, int st) {
