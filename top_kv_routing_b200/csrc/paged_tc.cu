@@ -149,6 +149,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
 __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
@@ -190,11 +196,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Adds the values that are not finite of the page tiles that were cleared of them (those a row
-// of the pair does not see in full), as far as this row sees them, to its stored output.
+// The first page row of the 16-row pieces that some row of the pair does not see in full: from
+// there on values that are not finite are taken out of the tiles.
+__device__ __forceinline__ int first_partial(const Unit& x) { return max(0, x.lim0) & ~15; }
+
+// Adds the values that were taken out, as far as this row sees them, to its stored output.
 __device__ __noinline__ void add_not_finite(const Attend& a, const Unit& x, int seen, __nv_bfloat16* out) {
   const int page = 1 << a.log2_page;
-  for (int k = max(0, x.lim0) / kTile * kTile; k < seen; ++k) {
+  for (int k = first_partial(x); k < seen; ++k) {
     const int id = a.page_table[(int64_t)x.e * a.max_pages + (k >> a.log2_page)];
     if (id < 0 || id >= a.NP) continue;
     const int64_t row = ((((((int64_t)x.l * a.NP + id) * 2 + 1) * a.H + x.h)) << a.log2_page) + (k & (page - 1));
@@ -777,10 +786,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       __syncwarp();
       // Values that are not finite must not reach the rows that do not see them (0 x inf is NaN):
       // they are taken out, and the unit's rows add what they see of them at the end.
-      if (BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0) {
-        bool any = false;
-        for (int i0 = 0; i0 < rows; i0 += 16) {  // 16 rows: 8 pieces of 16 bytes a lane
-          uint32_t w[8][4];
+      // (One pass that only looks, 16 rows at a time, and as a rule finds nothing: adding a
+      // step to an exponent of all ones carries into the sign's place.)
+      if (BLOCK && tile >= x.mt) {
+        for (int i0 = max(0, first_partial(x) - (tile - x.mt) * kTile); i0 < rows; i0 += 16) {
+          uint32_t w[8][4], found = 0u;
           const uint32_t from = vt + (uint32_t)(i0 * 128 + lane * 16);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
@@ -789,22 +799,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
                          : "r"(from + (uint32_t)((e >> 2) * kHalfBytes + (e & 3) * 512))
                          : "memory");
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            bool bad = false;
+          for (int e = 0; e < 8; ++e)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              if ((w[e][v] & 0x7F80u) == 0x7F80u) w[e][v] &= 0xFFFF0000u, bad = true;
-              if ((w[e][v] & 0x7F800000u) == 0x7F800000u) w[e][v] &= 0x0000FFFFu, bad = true;
-            }
-            if (bad)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               from + (uint32_t)((e >> 2) * kHalfBytes + (e & 3) * 512)),
-                           "r"(w[e][0]), "r"(w[e][1]), "r"(w[e][2]), "r"(w[e][3])
-                           : "memory");
-            any |= bad;
+            for (int v = 0; v < 4; ++v) found |= ((w[e][v] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+          if (__any_sync(0xffffffffu, found != 0u)) {
+            for (int e = 0; e < 8; ++e)
+              for (int v = 0; v < 4; ++v) {
+                const uint32_t to = from + (uint32_t)((e >> 2) * kHalfBytes + (e & 3) * 512 + v * 4);
+                uint32_t y;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(to) : "memory");
+                if ((y & 0x7F80u) == 0x7F80u) y &= 0xFFFF0000u;
+                if ((y & 0x7F800000u) == 0x7F800000u) y &= 0x0000FFFFu;
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(y) : "memory");
+              }
+            if (lane == 0) *const_cast<volatile int*>(&tb.units[un % kUnits].poison) = 1;
           }
         }
-        if (__any_sync(0xffffffffu, any) && lane == 0) *const_cast<volatile int*>(&tb.units[un % kUnits].poison) = 1;
       }
       __threadfence_block();
       fence_async_smem();
@@ -904,6 +914,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (lane == 0) {
           tb.units[un % kUnits] = x;
           mbar_arrive(smem_u32(&u_full[un % kUnits]));
+          // its queries into L2, so that they arrive soon once their place is free
+          for (int st = 0; st < 2; ++st)
+            if (x.t1[st] > x.t0[st] && (st == 0 || x.shared)) {
+              tma_prefetch_4d(&tm_q, 0, x.h * G, x.tok[st], x.l);
+              tma_prefetch_4d(&tm_q, kHalf, x.h * G, x.tok[st], x.l);
+            }
         }
         __syncwarp();
       }
