@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "msa_paged.h"
 
@@ -67,6 +69,19 @@ inline size_t memory_bytes(int64_t rows, int splits) {
 cudaError_t launch_memory(const Attend& a, int max_splits, cudaStream_t s);
 // The same kernel's block form: memory and pages of long blocks of new tokens, the whole result.
 cudaError_t launch_blocks(const Attend& a, cudaStream_t s);
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; `done` remembers the
+// devices on which it may (the call costs a microsecond of every launch otherwise).
+inline cudaError_t allow_shared_memory(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // ---- device helpers
 

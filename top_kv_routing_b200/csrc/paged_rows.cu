@@ -623,7 +623,8 @@ template <int G, int NR, bool PART>
 cudaError_t launch_rows_t(const Attend& a, int memory_splits, cudaStream_t s) {
   constexpr int kSmem = kRingBytes + (int)sizeof(Tables);
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(rows_kernel<G, NR, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(rows_kernel<G, NR, PART>), kSmem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(std::min(msa::sm_count(), kRowCtas), 1, 1);

@@ -1002,7 +1002,8 @@ cudaError_t launch_tiles_t(const Attend& a, int max_splits, cudaStream_t s) {
   if (BLOCK && !make_kv_map(&tm_pages, a.pages, ((uint64_t)a.L * a.NP * 2 * a.H) << a.log2_page,
                             std::min(kBox, 1 << a.log2_page)))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(tile_kernel<G, BLOCK>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTc);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_shared_memory(reinterpret_cast<const void*>(tile_kernel<G, BLOCK>), kSmemTc, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(msa::sm_count(), 1, 1);
