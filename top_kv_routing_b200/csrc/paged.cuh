@@ -50,7 +50,8 @@ constexpr size_t kWsEnd = kWsPart + (size_t)2 * kRowWorkers * 16 * kD * sizeof(f
 cudaError_t launch_rows(const Attend& a, int memory_splits, cudaStream_t s);
 
 // ---- the memory kernel (paged_tc.cu): all rows of a group at once, tcgen05.  Its output, per
-// partial slot and row (layer, token, query head): the unnormalised output, then (after all
+// partial slot and row (layer, token, query head): the unnormalised output (of every 16
+// dims in the order 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15, the row kernel's), then (after all
 // of them) the row's maximum (log2 domain) and sum.  A group of at most one row tile (128 / G
 // tokens) has 2 x splits slots, others `splits`.
 constexpr size_t kWsMemory = kWsEnd;

@@ -46,12 +46,12 @@ constexpr int kUnitTicks = 6; // what a unit costs beyond its tiles (queries in,
 // The tables of the batch in shared memory.
 struct Tables {
   int64_t scan[kMaxSeqs + 1];  // tiles of sequences before b, in units of one (layer, key head)
-  int tok0[kMaxSeqs];          // first token
+  int tok0[kMaxSeqs + 1];      // first token (the offsets as given)
   int n[kMaxSeqs];             // new tokens
   int len[kMaxSeqs];           // rows with the new tokens, as given
   int grp[kMaxSeqs];           // group, or -1
-  int mt[kMaxSeqs];            // memory tiles (the longest layer's)
-  int gmt[kMaxSeqs];           // the same by group (PART: partial slots per split)
+  int gmt[kMaxSeqs];           // memory tiles of a group's longest layer (PART: partial slots per split)
+  int goff[kMaxSeqs + 1];      // group offsets
   int64_t warp_sum[kRowWarps];
 };
 
@@ -92,53 +92,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!PART) wait_for_earlier_kernels();
   let_next_kernel_start();
 
-  // ---- tables
+  // ---- tables (all they read is loaded before the first barrier)
+  for (int g = tid; g <= a.NG; g += kThreads) {
+    tb.goff[g] = a.NG > 0 ? a.group_offsets[g] : 0;
+    if (g < a.NG) tb.gmt[g] = 0;
+  }
   for (int b = tid; b < a.B; b += kThreads) {
     int lo, n;
     if (!sequence_tokens(a.q_offsets, b, a.T, lo, n) && blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
     const int len = a.seq_len[b];
     if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
     tb.tok0[b] = lo;
+    if (b == a.B - 1) tb.tok0[a.B] = a.q_offsets[a.B];
     tb.n[b] = n;
     tb.len[b] = len;
     tb.grp[b] = -1;
-    tb.mt[b] = 0;
+  }
+  // the most memory tiles of any layer, by group (a thread's first entries are loaded ahead)
+  int ml[2];
+  if (!PART) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) ml[i] = tid + i * kThreads < a.NG * a.L ? a.mem_len[tid + i * kThreads] : 0;
   }
   __syncthreads();
-  const bool groups_ok = group_offsets_usable(a, tid, kThreads);  // (a barrier for all threads)
+  bool ok = true;
+  for (int g = tid; g < a.NG; g += kThreads) {
+    const int s = tb.goff[g], e = tb.goff[g + 1];
+    ok &= s >= 0 && e >= s && e <= a.B;
+  }
+  if (!PART) {
+    for (int i = tid; i < a.NG * a.L; i += kThreads) {
+      int m = i == tid ? ml[0] : i == tid + kThreads ? ml[1] : a.mem_len[i];
+      if (m > a.M_max) {
+        if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
+        m = a.M_max;
+      }
+      if (m > 0) atomicMax(&tb.gmt[i / a.L], (m + kTileKeys - 1) / kTileKeys);
+    }
+  }
+  const bool groups_ok = __syncthreads_and(ok);
   if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
   for (int gr = warp; gr < a.NG && groups_ok; gr += kRowWarps) {
-    const int s = a.group_offsets[gr], e = a.group_offsets[gr + 1];
-    int most = 0;
+    const int s = tb.goff[gr], e = tb.goff[gr + 1];
     if (PART) {
       // partial slots per split: two where the group's rows fit one row tile, none where the
       // memory kernel left the group out
-      int lo, n;
-      if (group_tokens(a, gr, lo, n)) most = n <= 128 / G ? 2 : 1;
-      for (int b = s + lane; b < e; b += 32)
-        if (tb.tok0[b] >= lo && tb.tok0[b] + tb.n[b] <= lo + n) tb.grp[b] = gr;
+      const int lo = tb.tok0[s], hi = tb.tok0[e];
+      const bool in = lo >= 0 && hi >= lo && hi <= a.T;
+      for (int b = s + lane; b < e && in; b += 32)
+        if (tb.tok0[b] >= lo && tb.tok0[b] + tb.n[b] <= hi) tb.grp[b] = gr;
+      if (lane == 0) tb.gmt[gr] = !in ? 0 : hi - lo <= 128 / G ? 2 : 1;
     } else {
-      for (int l = lane; l < a.L; l += 32) {
-        int m = a.mem_len[(int64_t)gr * a.L + l];
-        if (m > a.M_max) {
-          if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
-          m = a.M_max;
-        }
-        most = max(most, m);
-      }
-      most = (__reduce_max_sync(0xffffffffu, most) + kTileKeys - 1) / kTileKeys;
       for (int b = s + lane; b < e; b += 32) tb.grp[b] = gr;
     }
-    if (lane == 0) tb.gmt[gr] = most;
   }
-  __syncthreads();
-  for (int b = tid; b < a.B; b += kThreads) tb.mt[b] = PART || tb.grp[b] < 0 ? 0 : tb.gmt[tb.grp[b]];
   __syncthreads();
   // tiles of sequence b per (layer, key head): row tiles x key tiles (at least one, so that a
   // unit without any key still writes its zeros)
-  auto key_tiles = [&](int b) -> int {
+  auto memory_tiles = [&](int b) -> int { return PART || tb.grp[b] < 0 ? 0 : tb.gmt[tb.grp[b]]; };
+  auto key_tiles = [&](int b, int mt) -> int {
     const int64_t len = min((int64_t)max(tb.len[b], 0), cap);
-    return max(1, tb.mt[b] + (int)((len + kTileKeys - 1) / kTileKeys));
+    return max(1, mt + (int)((len + kTileKeys - 1) / kTileKeys));
   };
   auto row_tiles = [&](int b) -> int { return (tb.n[b] + kTok - 1) / kTok; };
   {
@@ -148,7 +162,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kPer; ++i) {
       const int b = tid * kPer + i;
       v[i] = sum;
-      if (b < a.B) sum += (int64_t)row_tiles(b) * (key_tiles(b) + kUnitTicks);
+      if (b < a.B) {
+        sum += (int64_t)row_tiles(b) * (key_tiles(b, memory_tiles(b)) + kUnitTicks);
+      }
     }
     int64_t inc = sum;
 #pragma unroll
@@ -173,7 +189,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int workers = gridDim.x * kRowWarps;
   const int worker = blockIdx.x * kRowWarps + warp;
   const int64_t total = tb.scan[a.B] * LH;
-  const int64_t per = max((int64_t)kMinTiles, (total + workers - 1) / workers);
+  // (64-bit divisions cost hundreds of cycles before the first load)
+  auto divide = [](int64_t x, int64_t y) -> int64_t {
+    return (uint64_t)(x | y) >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
+  };
+  const int64_t per = max((int64_t)kMinTiles, divide(total + workers - 1, workers));
   const int64_t w0 = worker * per, w1 = min(total, w0 + per);
   if (w0 >= w1) {
     if (PART) wait_for_earlier_kernels();
@@ -194,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto set_sequence = [&](Cursor& c) {
     c.RT = row_tiles(c.b);
-    c.nt = key_tiles(c.b);
-    c.mt = tb.mt[c.b];
+    c.mt = memory_tiles(c.b);
+    c.nt = key_tiles(c.b, c.mt);
     c.len = (int)min((int64_t)max(tb.len[c.b], 0), cap);
     c.cut = max(tb.len[c.b], 0) - tb.n[c.b];
   };
@@ -228,9 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     c.b = lo;
     set_sequence(c);
     const int64_t rem = w0 - tb.scan[lo] * LH, unit = c.nt + kUnitTicks, each = c.RT * unit;
-    c.lh = (int)(rem / each);
+    c.lh = (int)divide(rem, each);
     const int64_t in = rem - c.lh * each;
-    c.rt = (int)(in / unit);
+    c.rt = (int)divide(in, unit);
     c.j = (int)(in - (int64_t)c.rt * unit);
     set_layer(c);
     if (c.j >= c.nt) {  // behind the unit's last tile
@@ -496,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u0 < w0 || u1 > w1) {
         // a cut unit: pieces belong to workers first .. last; the piece at a worker's start
         // (a unit begun before it) goes to slot 2 w, the one it begins to slot 2 w + 1
-        const int first = (int)(u0 / per), last = (int)((u1 - 1) / per);
+        const int first = (int)divide(u0, per), last = (int)divide(u1 - 1, per);
         float2* stat = reinterpret_cast<float2*>(a.ws + kWsStat);
         float* part = reinterpret_cast<float*>(a.ws + kWsPart);
         int* counter = reinterpret_cast<int*>(a.ws + kWsCounters) + first;
@@ -559,33 +579,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* part = reinterpret_cast<const float*>(a.ws + kWsMemory);
         const float2* stat =
             reinterpret_cast<const float2*>(a.ws + kWsMemory + memory_part_bytes(all_rows, max_splits));
+        // With fewer than eight rows several of the eight quads of lanes share a row: of its
+        // `share` quads, number `mine` takes the slots mine, mine + share, ...
+        const int valid = min(kTok, tb.n[c.b] - c.rt * kTok) * G;
+        const int vr = valid > 4 ? 8 : valid > 2 ? 4 : valid;
+        const int share = 8 / vr, mine = g / vr;
 #pragma unroll
         for (int v = 0; v < NR; ++v) {
-          const int r = g + 8 * v;
-          if (row_token(r) < tb.n[c.b]) {
-            const int64_t row = row_at(r) / kD;
-            float top = m[v];
-            for (int s = 0; s < slots; ++s) top = fmaxf(top, __ldcg(&stat[s * all_rows + row]).x);
-            const float base = top == -INFINITY ? 0.f : top;
-            const float own = ex2_ftz(m[v] - base);
-            sum[v] *= own;
+          if (v > 0 && valid <= 8) break;
+          const int r = (g & (vr - 1)) + 8 * v;
+          const bool has = r < valid;
+          const int64_t row = has ? row_at(r) / kD : 0;
+          const int n_slots = has ? slots : 0;
+          float top = __shfl_sync(0xffffffffu, m[v], ((g & (vr - 1)) << 2) | t);
+          for (int s = mine * 4 + t; s < n_slots; s += 4 * share) top = fmaxf(top, __ldcg(&stat[s * all_rows + row]).x);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          for (int o2 = 4 * vr; o2 < 32; o2 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+          const float base = top == -INFINITY ? 0.f : top;
+          const float own = ex2_ftz(m[v] - base);
+          sum[v] = mine == 0 ? sum[v] * own : 0.f;
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            o[n][2 * v] = mine == 0 ? o[n][2 * v] * own : 0.f;
+            o[n][2 * v + 1] = mine == 0 ? o[n][2 * v + 1] * own : 0.f;
+          }
+          const float* src = part + row * kD + 4 * t;
+#pragma unroll 2
+          for (int s = mine; s < n_slots; s += share) {
+            const float2 ml = __ldcg(&stat[s * all_rows + row]);
+            const bool use = ml.y != 0.f;  // (an empty split writes no output)
+            const float f = use ? ex2_ftz(ml.x - base) : 0.f;
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              x[k] = use ? __ldcg(reinterpret_cast<const float4*>(src + s * all_rows * kD + 16 * k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            sum[v] = fmaf(f, ml.y, sum[v]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              o[2 * k][2 * v] = fmaf(f, x[k].x, o[2 * k][2 * v]);
+              o[2 * k][2 * v + 1] = fmaf(f, x[k].y, o[2 * k][2 * v + 1]);
+              o[2 * k + 1][2 * v] = fmaf(f, x[k].z, o[2 * k + 1][2 * v]);
+              o[2 * k + 1][2 * v + 1] = fmaf(f, x[k].w, o[2 * k + 1][2 * v + 1]);
+            }
+          }
+          for (int o2 = 4 * vr; o2 < 32; o2 <<= 1) {
+            sum[v] += __shfl_xor_sync(0xffffffffu, sum[v], o2);
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
-              o[n][2 * v] *= own;
-              o[n][2 * v + 1] *= own;
-            }
-            for (int s = 0; s < slots; ++s) {
-              const float2 ml = __ldcg(&stat[s * all_rows + row]);
-              if (ml.y == 0.f) continue;  // (an empty split writes no output)
-              const float f = ex2_ftz(ml.x - base);
-              sum[v] = fmaf(f, ml.y, sum[v]);
-              const float* src = part + (s * all_rows + row) * kD + 2 * t;
-#pragma unroll
-              for (int n = 0; n < 16; ++n) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(src + 8 * n));
-                o[n][2 * v] = fmaf(f, x.x, o[n][2 * v]);
-                o[n][2 * v + 1] = fmaf(f, x.y, o[n][2 * v + 1]);
-              }
+              o[n][2 * v] += __shfl_xor_sync(0xffffffffu, o[n][2 * v], o2);
+              o[n][2 * v + 1] += __shfl_xor_sync(0xffffffffu, o[n][2 * v + 1], o2);
             }
           }
         }

@@ -755,7 +755,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
         } else if (mine && n > 0) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) st_global_v8(part + row * kD + 32 * c + 8 * e, *reinterpret_cast<uint32_t(*)[8]>(&o[8 * e]));
+          for (int e = 0; e < 4; ++e) {
+            // (the row kernel's order: of every 16 dims, 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15)
+            const int d = 16 * (e >> 1) + 4 * (e & 1);
+            const uint32_t w[8] = {o[d], o[d + 1], o[d + 8], o[d + 9], o[d + 2], o[d + 3], o[d + 10], o[d + 11]};
+            st_global_v8(part + row * kD + 32 * c + 8 * e, w);
+          }
         }
       }
       if (BLOCK && mine && poisoned) add_not_finite(a, x, seen, a.out + row * kD);
