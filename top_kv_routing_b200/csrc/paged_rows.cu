@@ -16,10 +16,11 @@
 // Each warp streams its tiles through its own 3-stage cp.async ring in shared memory (16 K
 // rows and 16 V rows a stage, 16-byte chunks XOR-swizzled by row so ldmatrix is
 // conflict-free), running on from unit to unit.  Per tile: S = Q K^T and O += P V as
-// m16n8k16 (bf16 in, fp32 accumulate).  The queries are exact bf16 operands; the weights are
-// split into a bf16 value and a bf16 residual (about 16 bits), so that only the output's own
-// rounding is left.  With R = 8 the residuals ride in the MMA's spare rows, with R = 16 they
-// take a second MMA.  Online softmax per row in the log2 domain.
+// m16n8k16 (bf16 in, fp32 accumulate).  The queries are exact bf16 operands.  With R = 8 the
+// weights are split into a bf16 value and a bf16 residual (about 16 bits), which rides in the
+// MMA's spare rows; with R = 16 they are rounded to bf16 (half a step, 2^-9 of each, as in the
+// tile kernel), since a residual would double the PV's MMAs.  Online softmax per row in the log2
+// domain, the running maximum raised (and O rescaled) only when a score exceeds it by 2^8.
 //
 // A unit that lies inside one warp's piece is written out at its end.  A unit cut between
 // warps leaves (max, sum, unnormalised output) per piece in the workspace; the last warp to
@@ -41,6 +42,7 @@ constexpr int kRowBytes = kD * 2;
 constexpr int kStageBytes = 2 * kTileKeys * kRowBytes;  // 16 K rows, then 16 V rows
 constexpr int kRingBytes = kRowWarps * kStages * kStageBytes;
 constexpr int kMinTiles = 2;  // tiles per warp below which a unit is not cut further
+constexpr float kHeadroom = 8.0f; // log2 growth of a row's maximum tolerated before rescaling
 constexpr int kUnitTicks = 6; // what a unit costs beyond its tiles (queries in, join, output), in tiles
 
 // The tables of the batch in shared memory.
@@ -414,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx = fmaxf(fmaxf(pr[v][0], pr[v][1]), fmaxf(pr[v][2], pr[v][3]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(m[v], mx);
+        const float m_new = mx > m[v] + kHeadroom ? mx : m[v];
         const float base = m_new == -INFINITY ? 0.f : m_new;  // (a row that has seen no key yet)
-        alpha[v] = ex2_ftz(m[v] - base);                      // 0 while m is still -inf
+        alpha[v] = m_new == m[v] ? 1.f : ex2_ftz(m[v] - base);  // 0 while m is still -inf
 #pragma unroll
         for (int u = 0; u < 4; ++u) pr[v][u] = ex2_ftz(pr[v][u] - base);
         lsum[v] = fmaf(lsum[v], alpha[v], (pr[v][0] + pr[v][1]) + (pr[v][2] + pr[v][3]));
@@ -433,15 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // A fragments of the weights: {row g keys 2t.., row g + 8 keys 2t.., the same for keys + 8}
-      uint32_t pa[4], pl[4];
+      uint32_t pa[4];
       if (NR == 1) {  // residuals in rows 8..15
         split_pair(pr[0][0], pr[0][1], pa[0], pa[1]);
         split_pair(pr[0][2], pr[0][3], pa[2], pa[3]);
       } else {
-        split_pair(pr[0][0], pr[0][1], pa[0], pl[0]);
-        split_pair(pr[NR - 1][0], pr[NR - 1][1], pa[1], pl[1]);
-        split_pair(pr[0][2], pr[0][3], pa[2], pl[2]);
-        split_pair(pr[NR - 1][2], pr[NR - 1][3], pa[3], pl[3]);
+        pa[0] = msa::float2_to_bf16x2(pr[0][0], pr[0][1]);
+        pa[1] = msa::float2_to_bf16x2(pr[NR - 1][0], pr[NR - 1][1]);
+        pa[2] = msa::float2_to_bf16x2(pr[0][2], pr[0][3]);
+        pa[3] = msa::float2_to_bf16x2(pr[NR - 1][2], pr[NR - 1][3]);
       }
       const int vrow = kTileKeys + (lane & 7) + 8 * ((lane >> 3) & 1);
       // O += P V, in the rows of token `only` alone if that is >= 0
@@ -458,7 +460,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             float(&d)[4] = o[2 * i2 + u];
             float x[4] = {d[0], d[1], d[2], d[3]};
             mma_bf16(x, pa, v[2 * u], v[2 * u + 1]);
-            if (NR == 2) mma_bf16(x, pl, v[2 * u], v[2 * u + 1]);
             d[0] = r0 ? x[0] : d[0];
             d[1] = r0 ? x[1] : d[1];
             d[2] = r1 ? x[2] : d[2];
