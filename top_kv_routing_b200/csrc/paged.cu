@@ -66,17 +66,20 @@ const RopeFreq& rope_freq(float theta) {
 }
 
 // ---------------------------------------------------------------------------- append
-// CTA (token tile, layer): warp w < TOK finds its token's sequence (a 32-way search of the
-// offsets), its page slot, and the 64 angles of its position; then eight threads per head
-// row rotate (query and key heads) or copy (value heads) 8 + 8 elements each.  The first
-// rows are loaded before the position is known.  Bound by HBM: every byte moves once.
+// CTA (token, run of layers): warp 0 finds the token's sequence (a 32-way search of the offsets),
+// its page slot and the 64 angles of its position, once for all layers of the run; then eight
+// threads per head row rotate (query and key heads) or copy (value heads) 8 + 8 elements each.
+// The first rows are loaded before the position is known and the next before the ones at hand are
+// stored.  Bound by HBM: every byte moves once.
 constexpr int kAppendThreads = 256;
+constexpr int kAppendCtas = 148 * 8;  // runs of layers are as long as leaves so many CTAs
 
 struct AppendArgs {
   const void *q, *k, *v;
   int64_t q_stride, k_stride, v_stride;
   const int32_t* off;
-  int T, B, Hq, H;
+  int T, B, L, Hq, H;
+  int run;  // layers of a CTA
   __nv_bfloat16* pages;
   int NP, log2_page;
   const int32_t* table;
@@ -89,92 +92,102 @@ struct AppendArgs {
   RopeFreq rf;
 };
 
+// Eight elements as they lie in memory, and as floats.
+template <typename In>
 struct Eight {
-  float x[8];
+  uint4 w[sizeof(In) / 2];
 };
-__device__ __forceinline__ Eight load8(const __nv_bfloat16* p) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  Eight r;
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+template <typename In>
+__device__ __forceinline__ Eight<In> load8(const In* p) {
+  Eight<In> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(In) / 2; ++i)
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.w[i].x), "=r"(r.w[i].y), "=r"(r.w[i].z), "=r"(r.w[i].w)
+                 : "l"(reinterpret_cast<const uint4*>(p) + i));
+  return r;
+}
+__device__ __forceinline__ void floats(const Eight<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t u[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = msa::bf16x2_to_float2(u[e]);
-    r.x[2 * e] = f.x;
-    r.x[2 * e + 1] = f.y;
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
   }
-  return r;
 }
-__device__ __forceinline__ Eight load8(const float* p) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  return Eight{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+__device__ __forceinline__ void floats(const Eight<float>& r, float (&x)[8]) {
+  const uint32_t u[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(u[e]);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const Eight& r) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) =
-      make_uint4(msa::float2_to_bf16x2(r.x[0], r.x[1]), msa::float2_to_bf16x2(r.x[2], r.x[3]),
-                 msa::float2_to_bf16x2(r.x[4], r.x[5]), msa::float2_to_bf16x2(r.x[6], r.x[7]));
+      make_uint4(msa::float2_to_bf16x2(x[0], x[1]), msa::float2_to_bf16x2(x[2], x[3]),
+                 msa::float2_to_bf16x2(x[4], x[5]), msa::float2_to_bf16x2(x[6], x[7]));
 }
 
-template <typename In, int TOK>
+template <typename In>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ float2 s_cs[TOK][kHalf];
-  __shared__ int64_t s_row[TOK];   // element offset of the token's row in key head 0, or -1
-  __shared__ int s_own[TOK];       // the token belongs to a sequence
-  const int l = blockIdx.y, t0 = blockIdx.x * TOK;
+  __shared__ float2 s_cs[kHalf];
+  __shared__ int64_t s_row;  // element offset of the token's row in layer 0's key head 0, or -1
+  __shared__ int s_own;      // the token belongs to a sequence
+  const int t = blockIdx.x, l0 = blockIdx.y * a.run, nl = min(a.run, a.L - l0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   wait_for_earlier_kernels();
   let_next_kernel_start();
-  const int heads = a.Hq + 2 * a.H;
-  const int items = heads * 8;
   const int p = tid & 7;  // dims 8p .. 8p + 7 and 64 + 8p .. (kAppendThreads is a multiple of 8)
-
-  // row `idx / 8` of token t: a query, key or value head
-  auto source = [&](int t, int head) -> const In* {
-    const int64_t row = (int64_t)l * a.T + t;
-    if (head < a.Hq) return static_cast<const In*>(a.q) + row * a.q_stride + head * kD;
-    if (head < a.Hq + a.H) return static_cast<const In*>(a.k) + row * a.k_stride + (head - a.Hq) * kD;
-    return static_cast<const In*>(a.v) + row * a.v_stride + (head - a.Hq - a.H) * kD;
+  // this thread's rows: `head` of layer l0 + li (with no queries to rotate from the first key head on)
+  const int first = a.q_rot ? 0 : a.Hq, heads = a.Hq + 2 * a.H;
+  struct At {
+    int li, head;
   };
-  // with no queries to rotate the walk starts at the keys
-  const int first = a.q_rot ? 0 : a.Hq * 8;
-  int idx = first + tid, ti = 0;
-  auto wrap = [&]() {
-    while (idx >= items && ti < TOK) {
-      idx -= items - first;
-      ++ti;
+  auto wrap = [&](At x) -> At {
+    while (x.head >= heads && x.li < nl) {
+      x.head -= heads - first;
+      ++x.li;
     }
+    return x;
   };
-  wrap();
-  Eight lo, hi;
-  const bool have = ti < TOK && t0 + ti < a.T;
-  if (have) {
-    const In* src = source(t0 + ti, idx >> 3);
-    lo = load8(src + 8 * p);
-    hi = load8(src + kHalf + 8 * p);
-  }
-  if (warp < TOK) {
-    const int t = t0 + warp;
-    int b = t < a.T ? find_last(a.off, a.B, t, lane) : -1;
+  struct Row {
+    Eight<In> lo, hi;
+  };
+  auto load = [&](const At& x) -> Row {
+    const int64_t row = (int64_t)(l0 + x.li) * a.T + t;
+    const In* src;
+    if (x.head < a.Hq)
+      src = static_cast<const In*>(a.q) + row * a.q_stride + x.head * kD;
+    else if (x.head < a.Hq + a.H)
+      src = static_cast<const In*>(a.k) + row * a.k_stride + (x.head - a.Hq) * kD;
+    else
+      src = static_cast<const In*>(a.v) + row * a.v_stride + (x.head - a.Hq - a.H) * kD;
+    return Row{load8(src + 8 * p), load8(src + kHalf + 8 * p)};
+  };
+  auto next = [&](const At& x) -> At { return wrap(At{x.li, x.head + kAppendThreads / 8}); };
+  At x = wrap(At{0, first + (tid >> 3)});
+  Row r;
+  if (x.li < nl) r = load(x);
+  if (warp == 0) {
+    int b = find_last(a.off, a.B, t, lane);
     int b0 = 0, n = 0;
     if (b >= 0 && (!sequence_tokens(a.off, b, a.T, b0, n) || t < b0 || t >= b0 + n)) b = -1;
     int64_t row = -1;
     if (b >= 0) {
-      const long long r = (long long)a.seq_len[b] - n + (t - b0);
-      const long long pos = (long long)a.rope_pos_offset + (a.pos_offset ? (long long)a.pos_offset[b] : 0ll) + r;
+      const long long i = (long long)a.seq_len[b] - n + (t - b0);
+      const long long pos = (long long)a.rope_pos_offset + (a.pos_offset ? (long long)a.pos_offset[b] : 0ll) + i;
       uint32_t err = 0u;
-      if (r < 0) {
+      if (i < 0) {
         err = MSA_DEVERR_BAD_OFFSETS;
-      } else if ((r >> a.log2_page) >= a.max_pages) {
+      } else if ((i >> a.log2_page) >= a.max_pages) {
         err = MSA_DEVERR_LOCAL_FULL;
       } else {
-        const int page = a.table[(int64_t)b * a.max_pages + (r >> a.log2_page)];
-        if (page < 0 || page >= a.NP) {
+        const int page = a.table[(int64_t)b * a.max_pages + (i >> a.log2_page)];
+        if (page < 0 || page >= a.NP)
           err = MSA_DEVERR_BAD_PAGE;
-        } else {
-          row = ((((int64_t)l * a.NP + page) * 2 * a.H) << a.log2_page) + (r & ((1ll << a.log2_page) - 1));
-          row *= kD;
-        }
+        else
+          row = ((((int64_t)page * 2 * a.H) << a.log2_page) + (i & ((1ll << a.log2_page) - 1))) * kD;
       }
-      if (err && lane == 0 && l == 0) msa::set_err(a.dev_err, err);
+      if (err && lane == 0 && l0 == 0) msa::set_err(a.dev_err, err);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int j = lane + 32 * e;
@@ -182,55 +195,52 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         const int top = (int)(((unsigned long long)pos * a.rf.step[j]) >> 32);
         float sn, c;
         sincospif((float)top * 4.656612873077392578125e-10f, &sn, &c);
-        s_cs[warp][j] = make_float2(c, sn);
+        s_cs[j] = make_float2(c, sn);
       }
     }
     if (lane == 0) {
-      s_row[warp] = row;
-      s_own[warp] = b >= 0;
+      s_row = row;
+      s_own = b >= 0;
     }
-  } else if (blockIdx.x == 0 && l == 0) {
+  } else if (blockIdx.x == 0 && l0 == 0) {
     // the first CTA's other warps check all offsets
-    for (int b = tid - 32 * TOK; b < a.B; b += kAppendThreads - 32 * TOK) {
+    for (int b = tid - 32; b < a.B; b += kAppendThreads - 32) {
       int b0, n;
       if (!sequence_tokens(a.off, b, a.T, b0, n)) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
     }
   }
   __syncthreads();
-  bool loaded = have;
-  while (ti < TOK && t0 + ti < a.T) {
-    const int head = idx >> 3;
-    if (s_own[ti]) {
-      if (!loaded) {
-        const In* src = source(t0 + ti, head);
-        lo = load8(src + 8 * p);
-        hi = load8(src + kHalf + 8 * p);
-      }
-      if (head < a.Hq + a.H) {
-        Eight rl, rh;
+  if (!s_own) return;
+  const int64_t row = s_row;
+  while (x.li < nl) {
+    const At y = next(x);
+    Row ahead;
+    if (y.li < nl) ahead = load(y);
+    float lo[8], hi[8];
+    floats(r.lo, lo);
+    floats(r.hi, hi);
+    if (x.head < a.Hq + a.H) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 c = s_cs[ti][8 * p + e];
-          rl.x[e] = lo.x[e] * c.x - hi.x[e] * c.y;
-          rh.x[e] = hi.x[e] * c.x + lo.x[e] * c.y;
-        }
-        lo = rl;
-        hi = rh;
-      }
-      __nv_bfloat16* dst = nullptr;
-      if (head < a.Hq) {
-        dst = a.q_rot + (((int64_t)l * a.T + t0 + ti) * a.Hq + head) * kD;
-      } else if (s_row[ti] >= 0) {  // key heads, then value heads: consecutive [page][128] blocks
-        dst = a.pages + s_row[ti] + ((int64_t)(head - a.Hq) << a.log2_page) * kD;
-      }
-      if (dst) {
-        store8(dst + 8 * p, lo);
-        store8(dst + kHalf + 8 * p, hi);
+      for (int e = 0; e < 8; ++e) {
+        const float2 c = s_cs[8 * p + e];
+        const float rl = lo[e] * c.x - hi[e] * c.y;
+        hi[e] = hi[e] * c.x + lo[e] * c.y;
+        lo[e] = rl;
       }
     }
-    loaded = false;
-    idx += kAppendThreads;
-    wrap();
+    __nv_bfloat16* dst = nullptr;
+    const int64_t l = l0 + x.li;
+    if (x.head < a.Hq) {
+      dst = a.q_rot + ((l * a.T + t) * a.Hq + x.head) * kD;
+    } else if (row >= 0) {  // key heads, then value heads: consecutive [page][128] blocks
+      dst = a.pages + row + (((l * a.NP * 2 * a.H + (x.head - a.Hq)) << a.log2_page) * kD);
+    }
+    if (dst) {
+      store8(dst + 8 * p, lo);
+      store8(dst + kHalf + 8 * p, hi);
+    }
+    x = y;
+    r = ahead;
   }
 }
 
@@ -277,7 +287,7 @@ msa_status check_pages(const void* kv_pages, int32_t n_pages, int32_t page_size,
 }
 
 template <typename In>
-cudaError_t launch_append(const AppendArgs& a, int n_layers, cudaStream_t s) {
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kAppendThreads, 1, 1);
   cfg.stream = s;
@@ -286,8 +296,8 @@ cudaError_t launch_append(const AppendArgs& a, int n_layers, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(a.T, n_layers, 1);
-  return cudaLaunchKernelEx(&cfg, append_kernel<In, 1>, a);
+  cfg.gridDim = dim3(a.T, (a.L + a.run - 1) / a.run, 1);
+  return cudaLaunchKernelEx(&cfg, append_kernel<In>, a);
 }
 
 }  // namespace
@@ -328,6 +338,8 @@ extern "C" msa_status msa_paged_append(const void* q, const void* k_new, const v
   a.off = q_offsets;
   a.T = n_tokens;
   a.B = n_seqs;
+  a.L = n_layers;
+  a.run = (int)std::min<int64_t>(n_layers, std::max<int64_t>(1, (int64_t)n_tokens * n_layers / kAppendCtas));
   a.Hq = n_q_heads;
   a.H = n_kv_heads;
   a.pages = static_cast<__nv_bfloat16*>(kv_pages);
@@ -342,8 +354,7 @@ extern "C" msa_status msa_paged_append(const void* q, const void* k_new, const v
   a.dev_err = dev_err;
   a.rf = rope_freq(rope_theta);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  MSA_CUDA_TRY((in_dtype == MSA_F32 ? launch_append<float>(a, n_layers, s)
-                                    : launch_append<__nv_bfloat16>(a, n_layers, s)));
+  MSA_CUDA_TRY((in_dtype == MSA_F32 ? launch_append<float>(a, s) : launch_append<__nv_bfloat16>(a, s)));
   g_launches = 1;
   return msa_ok();
 }
