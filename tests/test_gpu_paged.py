@@ -301,3 +301,178 @@ def test_agrees_with_the_single_query_decode_step():
     # the two differ by the rounding of the rotated query to bf16 and the two outputs' own
     a, b = x.out[:, 0].double(), out[0].double()
     assert (a - b).norm() / b.norm() <= 2 ** -7
+
+
+# ----------------------------------------------------------------------------- long blocks, many rows
+
+BLOCKS = {
+    # rows per sequence (new x G) from 64 on walk memory and pages in one kernel
+    "one short block": dict(new=[16], past=[0], H=1, G=4),
+    "edges of a tile pair": dict(new=[31, 32, 33, 63, 64, 65], past=[0, 127, 128, 1, 97, 64], H=2, G=4, page=32),
+    "one query head": dict(new=[127, 128, 129, 257], past=[0, 5, 130, 260], H=2, G=1, page=256, groups=[0, 4], mem=[129]),
+    "two query heads": dict(new=[64, 200], past=[100, 0], H=1, G=2, page=128, groups=[0, 1, 2], mem=[1, 128]),
+    "eight query heads": dict(new=[20, 50, 8], past=[200, 3, 77], H=2, G=8, groups=[0, 2], mem=[255]),
+    "empty memory": dict(new=[40, 40], past=[0, 30], H=1, G=4, groups=[0, 1, 2], mem=[0, 17]),
+    "layers of other lengths": dict(new=[50, 30], past=[20, 260], L=3, H=1, G=4, groups=[0, 2], mem=[[0, 128, 300]]),
+    "some without tokens": dict(new=[0, 90, 0, 1, 70], past=[3, 0, 0, 500, 33], H=1, G=4, groups=[1, 4], mem=[60],
+                                pad=5, lead=4),
+    "a long past": dict(new=[33], past=[3000], H=1, G=4, page=64, groups=[0, 1], mem=[700]),
+    "peaked": dict(new=[60, 45], past=[200, 3], H=1, G=4, groups=[0, 2], mem=[300], scale=8.0),
+    "sixteen key heads": dict(new=[40], past=[150], H=16, G=2, groups=[0, 1], mem=[140]),
+}
+
+MANY_ROWS = {
+    # groups of more than one, two, four row tiles; the memory split over few and many units
+    "one tile": dict(new=[1] * 32, past=[i for i in range(32)], H=1, G=4, groups=[0, 32], mem=[129]),
+    "a tile and a row": dict(new=[1] * 33, past=[2] * 33, H=1, G=4, groups=[0, 33], mem=[500]),
+    "pairs of tiles": dict(new=[1] * 150, past=[i % 40 for i in range(150)], H=2, G=4, groups=[0, 150], mem=[300]),
+    "groups of all sizes": dict(new=[1] * 100, past=[i % 23 for i in range(100)], L=2, H=2, G=8,
+                                groups=[0, 1, 3, 20, 37, 99], mem=[[5, 700], [64, 0], [0, 128], [256, 255], [33, 1]]),
+    "drafts of all lengths": dict(new=[i % 6 for i in range(60)], past=[7 * i % 50 for i in range(60)], H=2, G=4,
+                                  groups=[2, 30, 58], mem=[150, 400], pad=2, lead=1),
+    "many empty splits": dict(new=[1] * 20, past=[9] * 20, H=1, G=4, groups=[0, 10, 20], mem=[8000, 3]),
+}
+
+
+@pytest.mark.parametrize("name", list(BLOCKS) + list(MANY_ROWS))
+def test_attend_blocks_and_many_rows(name):
+    x = Batch(seed=21, **{**BLOCKS, **MANY_ROWS}[name])
+    launches = x.call_attend(msa)
+    assert launches == (1 if name in BLOCKS else 2)
+    x.check()
+    assert x.err.item() == 0
+    first = x.out.clone()
+    x.call_attend(msa)
+    assert torch.equal(first.view(torch.int16), x.out.view(torch.int16))
+
+
+@pytest.mark.parametrize("G,new", [(4, 70), (2, 140), (8, 33)])
+def test_values_that_are_not_finite_in_many_blocks(G, new):
+    # several units per SM, every one with rows that must not see the last token's values
+    B, H = 24, 4
+    x = Batch([new] * B, [(37 * b) % 150 for b in range(B)], L=2, H=H, G=G, page=32, groups=[0, B], mem=[130], seed=22)
+    last = [(x.ids[b][(p + new - 1) // 32], (p + new - 1) % 32) for b, p in enumerate(x.past)]
+    kept = []
+    for b, (page, slot) in enumerate(last):
+        kept.append(x.pages[:, page, 1, :, slot].clone())
+        x.pages[:, page, 1, :, slot, b % D] = float("inf") if b % 3 else float("nan")
+    x.call_attend(msa)
+    got = x.out.clone()
+    for b, (page, slot) in enumerate(last):
+        x.pages[:, page, 1, :, slot] = kept[b]
+    x.out.fill_(7.0)
+    x.call_attend(msa)
+    x.check()
+    ends = x.off[1:].long() - 1
+    rest = torch.ones(x.T, dtype=torch.bool, device="cuda")
+    rest[ends] = False
+    assert torch.equal(got[:, rest].view(torch.int16), x.out[:, rest].view(torch.int16))
+    for b in range(B):
+        row = got[:, ends[b]]
+        at = torch.arange(D, device="cuda") == b % D
+        assert (row[..., at].isnan().all() if b % 3 == 0 else (row[..., at] == float("inf")).all())
+        assert torch.equal(row[..., ~at].view(torch.int16), x.out[:, ends[b]][..., ~at].view(torch.int16))
+
+
+def test_block_device_conditions():
+    x = Batch([40, 40, 40], [60, 60, 60], H=2, G=4, page=32, groups=[0, 3], mem=[50], seed=23)
+    x.call_attend(msa)
+    good = x.out.clone()
+    x.check()
+    x.table[1, 1] = x.n_pages + 3               # rows 32..63 of sequence 1 are not seen
+    x.mem_len[0, 0] = 60                        # clamped to 50
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_PAGE | msa.MSA_DEVERR_CAPACITY
+    for b in (0, 2):
+        assert torch.equal(x.out[:, 40 * b:40 * b + 40].view(torch.int16), good[:, 40 * b:40 * b + 40].view(torch.int16))
+    want, tol = x.attend()
+    loc = x.rows(1, 100)
+    for i in (0, 17, 39):
+        keep = torch.tensor([r for r in range(61 + i) if not 32 <= r < 64], device="cuda")
+        k = torch.cat([x.mem[0, 0, 0, :, :50].double(), loc[0, 0][:, keep]], 1)
+        v = torch.cat([x.mem[0, 0, 1, :, :50].double(), loc[1, 0][:, keep]], 1)
+        s = torch.einsum("hgd,hkd->hgk", x.q[0, 40 + i].double().view(2, 4, D), k) * D ** -0.5
+        w = torch.einsum("hgk,hkd->hgd", torch.softmax(s, -1), v).reshape(8, D)
+        assert ((x.out[0, 40 + i].double() - w).abs() <= tol[0, 40 + i] + 2 ** -7 * w.abs()).all()
+    x.err.zero_()
+    x.mem_len[0, 0] = 50
+    x.off[2] = 4000                             # sequences 1 and 2 unusable: left as they were
+    x.out.fill_(7.0)
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_OFFSETS
+    assert (x.out[:, 40:] == 7.0).all()
+    assert torch.equal(x.out[:, :40].view(torch.int16), good[:, :40].view(torch.int16))
+
+
+def test_blocks_whose_first_rows_see_nothing():
+    x = Batch([50, 60], [0, 0], H=1, G=4, seed=24)
+    x.seq_len[0], x.seq_len[1] = 20, 0
+    x.call_attend(msa)
+    x.check()
+    assert (x.out[:, :30] == 0).all() and (x.out[:, 30:50] != 0).any() and (x.out[:, 50:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("with_q", [True, False])
+def test_append_of_many_tokens_and_layers(dtype, with_q):
+    # a CTA takes a run of layers of its token: runs that do not divide the layers
+    x = Batch([300, 1, 211, 170], [3, 60, 0, 31], L=7, H=2, G=4, page=64, pad=3, seed=25, dtype=dtype)
+    before, q_rot = x.pages.clone(), torch.full_like(x.out, 7.0)
+    off = torch.tensor([5, 0, 1000, 77], dtype=torch.int32, device="cuda")
+    q = x.q
+    if not with_q:
+        x.call_append(msa, off, 16, q_rot=q_rot)
+        once, x.q = x.pages.clone(), None
+        x.pages.copy_(before)
+        x.call_append(msa, off, 16)
+        assert torch.equal(once.view(torch.int16), x.pages.view(torch.int16))
+        x.q = q
+    else:
+        x.call_append(msa, off, 16, q_rot=q_rot)
+    _check_append(x, q_rot, before, off, 16)
+    assert (q_rot[:, -3:] == 7.0).all() and x.err.item() == 0
+
+
+def test_calls_follow_the_current_stream():
+    # captured from the current stream, without a stream argument: append, block form and memory form
+    x = Batch([70, 60], [0, 20], H=2, G=4, groups=[0, 2], mem=[100], seed=26)
+    y = Batch([1] * 12, [30] * 12, H=2, G=4, groups=[0, 12], mem=[100], seed=27)
+    for z in (x, y):
+        z.call_attend(msa)
+    q_rot = [torch.empty_like(z.out) for z in (x, y)]
+    raw = [z.q for z in (x, y)]
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        for z, r, w in zip((x, y), q_rot, raw):
+            z.q = w
+            z.call_append(msa, q_rot=r)
+            z.q = r
+            z.call_attend(msa)
+    for _ in range(2):
+        for z, w in zip((x, y), raw):
+            w.normal_()
+            z.k.normal_()
+            z.v.normal_()
+            z.out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        x.check()
+        y.check()
+
+
+def test_two_streams_with_their_own_workspaces():
+    xs = [Batch([1] * 40, [25] * 40, L=2, H=4, G=4, groups=[0, 40], mem=[900], seed=28),
+          Batch([50] * 6, [40] * 6, L=2, H=4, G=4, groups=[0, 6], mem=[500], seed=29),
+          Batch([1] * 9, [700] * 9, L=2, H=4, G=4, seed=30)]
+    for x in xs:
+        x.call_attend(msa)
+    torch.cuda.synchronize()
+    alone = [x.out.clone() for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(20):
+        for x, s in zip(xs, streams):
+            x.call_attend(msa, stream=s)
+    torch.cuda.synchronize()
+    for x, want in zip(xs, alone):
+        assert torch.equal(x.out.view(torch.int16), want.view(torch.int16)) and x.err.item() == 0
