@@ -82,7 +82,8 @@ msa_status msa_shared_attend_workspace_size(int32_t n_tokens, int32_t n_seqs, in
  *                 msa_paged_append)
  *   out[l][t][hq] = softmax(softmax_scale * <q_hq, K_j>) . V_j, key head h = hq / G, and 0
  *                   for a token that sees no key at all
- * (fp32 scores, maxima and sums; output rounded to bf16).
+ * (fp32 scores, maxima and sums; the weights may be rounded to bf16 for the tensor cores, the
+ * output is rounded to bf16).
  *   q       DEVICE bf16 [n_layers][n_tokens][n_q_heads][head_dim], already rotated (q_rot)
  *   mem_kv  DEVICE bf16 [n_groups][n_layers][2][n_kv_heads][max_mem_chunks][head_dim]
  *           (msa_gather_kv output of n_groups queries); mem_len DEVICE int32 [n_groups][n_layers];
@@ -95,12 +96,14 @@ msa_status msa_shared_attend_workspace_size(int32_t n_tokens, int32_t n_seqs, in
  *           next, of any sizes.  Calls that share a workspace must not overlap on the device.
  *   head_dim = 128; n_q_heads / n_kv_heads in {1, 2, 4, 8}; n_kv_heads <= 16; n_seqs <=
  *   MSA_PAGED_MAX_SEQS; n_groups <= n_seqs; softmax_scale > 0 and finite; q, mem_kv, kv_pages,
- *   out, workspace 16-byte aligned.
+ *   out, workspace 16-byte aligned; mem_kv and kv_pages hold fewer than 2^31 - 128 rows of
+ *   head_dim each (MSA_ERR_CAPACITY where a batch takes the tensor-core kernels beyond that).
  * Device conditions: mem_len > max_mem_chunks is clamped with MSA_DEVERR_CAPACITY; seq_len
  * past max_pages * page_size is clamped with MSA_DEVERR_LOCAL_FULL; rows of a page id outside
  * [0, n_pages) are not seen (MSA_DEVERR_BAD_PAGE); q_offsets or group_offsets that decrease or
  * leave their range set MSA_DEVERR_BAD_OFFSETS and such a sequence (its output left as it
- * was) or group (no memory) is skipped.
+ * was) or group (no memory) is skipped.  Waits inside the tensor-core kernel are bounded: a timeout
+ * sets MSA_DEVERR_TIMEOUT and leaves the output and the workspace undefined (zero it again).
  * Asynchronous on `stream`, graph-capturable, launched as programmatic dependents. */
 msa_status msa_shared_attend(const void* q, const int32_t* q_offsets, int32_t n_tokens, int32_t n_seqs,
                              int32_t n_layers, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
