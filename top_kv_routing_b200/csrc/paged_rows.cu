@@ -73,6 +73,11 @@ __device__ __forceinline__ bool not_finite(uint32_t st, int lane) {
   return bad;
 }
 
+// 16-byte global -> shared copy
+__device__ __forceinline__ void cp_async16_full(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
 // PART: the memory part comes from the memory kernel's partial results.
 template <int G, int NR, bool PART>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -94,27 +99,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!PART) wait_for_earlier_kernels();
   let_next_kernel_start();
 
-  // ---- tables (all they read is loaded before the first barrier)
-  for (int g = tid; g <= a.NG; g += kThreads) {
-    tb.goff[g] = a.NG > 0 ? a.group_offsets[g] : 0;
-    if (g < a.NG) tb.gmt[g] = 0;
+  // ---- tables (a thread's first entries of all they read are on their way at once)
+  const int g_first = a.NG > 0 && tid <= a.NG ? a.group_offsets[tid] : 0;
+  int lo_first = 0, hi_first = 0, len_first = 0;
+  if (tid < a.B) {
+    lo_first = a.q_offsets[tid];
+    hi_first = a.q_offsets[tid + 1];
+    len_first = a.seq_len[tid];
   }
-  for (int b = tid; b < a.B; b += kThreads) {
-    int lo, n;
-    if (!sequence_tokens(a.q_offsets, b, a.T, lo, n) && blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-    const int len = a.seq_len[b];
-    if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
-    tb.tok0[b] = lo;
-    if (b == a.B - 1) tb.tok0[a.B] = a.q_offsets[a.B];
-    tb.n[b] = n;
-    tb.len[b] = len;
-    tb.grp[b] = -1;
-  }
-  // the most memory tiles of any layer, by group (a thread's first entries are loaded ahead)
-  int ml[2];
+  int ml[2];  // memory rows of (group, layer)
   if (!PART) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) ml[i] = tid + i * kThreads < a.NG * a.L ? a.mem_len[tid + i * kThreads] : 0;
+  }
+  for (int g = tid; g <= a.NG; g += kThreads) {
+    tb.goff[g] = g == tid ? g_first : a.group_offsets[g];
+    if (g < a.NG) tb.gmt[g] = 0;
+  }
+  for (int b = tid; b < a.B; b += kThreads) {
+    const int lo = b == tid ? lo_first : a.q_offsets[b], hi = b == tid ? hi_first : a.q_offsets[b + 1];
+    const int len = b == tid ? len_first : a.seq_len[b];
+    const bool usable = lo >= 0 && hi >= lo && hi <= a.T;
+    const int n = usable ? hi - lo : 0;
+    if (!usable && blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+    if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
+    tb.tok0[b] = lo;
+    if (b == a.B - 1) tb.tok0[a.B] = hi;
+    tb.n[b] = n;
+    tb.len[b] = len;
+    tb.grp[b] = -1;
   }
   __syncthreads();
   bool ok = true;
@@ -268,6 +281,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int ids_b = -1, ids_win = -1, ids = 0;
   uint32_t bad = 0u;  // stages whose page id is unusable
 
+  // where this lane's 16 bytes of rows 2 u and 2 u + 1 go, beyond u x 512 bytes (u modulo 4)
+  uint32_t to[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    to[q] = (lane >> 4) * kRowBytes + (((lane & 15) ^ ((2 * q + (lane >> 4)) & 7)) << 4);
+
   auto issue = [&](int i) {
     const int stage = i % kStages;
     const __nv_bfloat16 *kp, *vp;
@@ -302,15 +321,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         vp = kp + ((int64_t)a.H << a.log2_page) * kD;
       }
     }
+    // instruction u: rows 2 u and 2 u + 1 of the keys, then of the values (a half warp each)
     const uint32_t st = my_ring + stage * kStageBytes;
-    const int chunk = lane & 15;
+    const __nv_bfloat16 *ks = kp + lane * 8, *vs = vp + lane * 8;
+    if (rows >= kTileKeys) {
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-      const int row = 2 * u + (lane >> 4);  // 0..15 K rows, 16..31 V rows
-      const int key = row & 15;
-      const bool ok = key < rows;
-      const __nv_bfloat16* src = (u < 8 ? kp : vp) + (ok ? key * kD + chunk * 8 : 0);
-      cp_async16(st + row * kRowBytes + ((chunk ^ (row & 7)) << 4), src, ok ? 16u : 0u);
+      for (int u = 0; u < 8; ++u) cp_async16_full(st + to[u & 3] + u * 512, ks + u * 256);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) cp_async16_full(st + to[u & 3] + (u + 8) * 512, vs + u * 256);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const bool ok = 2 * u + (lane >> 4) < rows;
+        cp_async16(st + to[u & 3] + u * 512, ok ? ks + u * 256 : kp, ok ? 16u : 0u);
+        cp_async16(st + to[u & 3] + (u + 8) * 512, ok ? vs + u * 256 : vp, ok ? 16u : 0u);
+      }
     }
     ++pat;
     if (++pc.j == pc.nt) {
