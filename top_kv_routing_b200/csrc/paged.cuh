@@ -108,17 +108,6 @@ __device__ __forceinline__ bool sequence_tokens(const int32_t* __restrict__ off,
   return ok;
 }
 
-// Whether the group offsets are non-decreasing within [0, B] (all threads of the block call it
-// and get the same answer).
-__device__ __forceinline__ bool group_offsets_usable(const Attend& a, int tid, int threads) {
-  bool ok = true;
-  for (int g = tid; g < a.NG; g += threads) {
-    const int s = a.group_offsets[g], e = a.group_offsets[g + 1];
-    ok &= s >= 0 && e >= s && e <= a.B;
-  }
-  return __syncthreads_and(ok);
-}
-
 // The packed tokens [lo, lo + n) of group g (whose offsets are usable); false where the
 // sequences' offsets are not.
 __device__ __forceinline__ bool group_tokens(const Attend& a, int g, int& lo, int& n) {

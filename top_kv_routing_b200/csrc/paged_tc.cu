@@ -267,13 +267,47 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     tmem_alloc<false>(smem_u32(&tb.tmem), kTmemCols);
     tmem_relinquish<false>();
   }
+  __syncthreads();  // (the shared variables are zeroed)
   wait_for_earlier_kernels();
   let_next_kernel_start();
 
   // ---- the batch: row-tile pairs, most key tiles
   const int n_entries = BLOCK ? a.B : a.NG, n_blocks = (n_entries + 31) / 32;
   const int64_t cap = (int64_t)a.max_pages << a.log2_page;
-  const bool groups_ok = group_offsets_usable(a, tid, kThreadsTc);  // (a barrier for all threads)
+  // what the batch needs is asked for at once: memory lengths, offsets of groups, tokens
+  int most = 0;
+  for (int i = tid; i < a.NG * a.L; i += kThreadsTc) most = max(most, a.mem_len[i]);
+  bool ok_here = true;  // the group offsets are non-decreasing within [0, B]
+  for (int g = tid; g < a.NG; g += kThreadsTc) {
+    const int s = a.group_offsets[g], e = a.group_offsets[g + 1];
+    ok_here &= s >= 0 && e >= s && e <= a.B;
+  }
+  auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
+  for (int k = warp; k < n_blocks; k += kWarpsTc) {
+    const int e = 32 * k + lane;
+    int lo = 0, n = 0;
+    if (e < n_entries) {
+      if (BLOCK) {
+        if (!sequence_tokens(a.q_offsets, e, a.T, lo, n) && blockIdx.x == 0)
+          msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+        if (blockIdx.x == 0 && n > 0 && a.seq_len[e] > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
+      } else {
+        const int s = a.group_offsets[e], f = a.group_offsets[e + 1];
+        if (s >= 0 && f >= s && f <= a.B) group_tokens(a, e, lo, n);
+      }
+    }
+    const int sum = __reduce_add_sync(0xffffffffu, pairs_of(n));
+    if (lane == 0) tb.scan[k] = sum;
+  }
+  if (most > a.M_max) {
+    if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
+    most = a.M_max;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) atomicMax(&tb.most, (most + kTile - 1) / kTile);
+  tc_fence_before();
+  const bool groups_ok = __syncthreads_and(ok_here);  // (where they are not, no group has a unit)
+  tc_fence_after();
   if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
   // tokens of entry e; false where they are unusable
   auto entry_tokens = [&](int e, int& lo, int& n) -> bool {
@@ -281,31 +315,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     lo = n = 0;
     return groups_ok && group_tokens(a, e, lo, n);
   };
-  auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
-  for (int k = warp; k < n_blocks; k += kWarpsTc) {
-    const int e = 32 * k + lane;
-    int lo = 0, n = 0;
-    if (e < n_entries && !entry_tokens(e, lo, n) && BLOCK && blockIdx.x == 0)
-      msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-    if (BLOCK && blockIdx.x == 0 && n > 0 && a.seq_len[e] > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
-    const int sum = __reduce_add_sync(0xffffffffu, pairs_of(n));
-    if (lane == 0) tb.scan[k] = sum;
-  }
-  {
-    int most = 0;
-    for (int i = tid; i < a.NG * a.L; i += kThreadsTc) most = max(most, a.mem_len[i]);
-    if (most > a.M_max) {
-      if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
-      most = a.M_max;
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 0) atomicMax(&tb.most, (most + kTile - 1) / kTile);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 0) {  // sums before each block
-    const int v = lane < n_blocks ? tb.scan[lane] : 0;
+  if (warp == 0) {  // sums before each block, and the split
+    const int v = lane < n_blocks && (BLOCK || groups_ok) ? tb.scan[lane] : 0;
     int inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -314,27 +325,36 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
     tb.scan[lane] = inc - v;
     if (lane == 31) tb.scan[32] = inc;
-  }
-  __syncthreads();
-  const int pairs = tb.scan[kBlocks];
-  if (tid == 0) {
     int best = 1;
     if (!BLOCK) {
-      // the split that finishes first, a unit costing its tiles and about two more
-      const int64_t units = (int64_t)pairs * LH;
-      int64_t cost = INT64_MAX;
-      for (int s = 1; s <= max_splits && s <= max(1, tb.most); ++s) {
-        const int64_t c = (units * s + gridDim.x - 1) / gridDim.x * ((tb.most + s - 1) / s + 2);
+      // the split that finishes first, a unit costing its tiles and about two more: a lane for
+      // every 32nd number of splits
+      const int64_t units = (int64_t)__shfl_sync(0xffffffffu, inc, 31) * LH;
+      const uint32_t most_tiles = max(1, tb.most);
+      float cost = INFINITY;
+      for (int s = lane + 1; s <= max_splits && s <= (int)most_tiles; s += 32) {
+        const float waves = ceilf((float)(units * s) / (float)gridDim.x);
+        const float c = waves * (float)((most_tiles + s - 1) / s + 2);
         if (c < cost) {
           cost = c;
           best = s;
         }
       }
-      if (blockIdx.x == 0) *reinterpret_cast<int*>(a.ws + kWsSplits) = best;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+        const int b = __shfl_xor_sync(0xffffffffu, best, o);
+        if (c < cost || (c == cost && b < best)) {
+          cost = c;
+          best = b;
+        }
+      }
+      if (lane == 0 && blockIdx.x == 0) *reinterpret_cast<int*>(a.ws + kWsSplits) = best;
     }
-    tb.splits = best;
+    if (lane == 0) tb.splits = best;
   }
   __syncthreads();
+  const int pairs = tb.scan[kBlocks];
   const int splits = tb.splits;
   const uint32_t tmem_base = tb.tmem;
   const int64_t n_units = (int64_t)pairs * LH * splits;
