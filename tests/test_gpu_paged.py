@@ -306,7 +306,8 @@ def test_agrees_with_the_single_query_decode_step():
 # ----------------------------------------------------------------------------- long blocks, many rows
 
 BLOCKS = {
-    # rows per sequence (new x G) from 64 on walk memory and pages in one kernel
+    # rows per sequence (new x G) from 64 on walk memory and pages in one kernel, where that makes
+    # enough units for the GPU (the test adds key heads and layers until it does)
     "one short block": dict(new=[16], past=[0], H=1, G=4),
     "edges of a tile pair": dict(new=[31, 32, 33, 63, 64, 65], past=[0, 127, 128, 1, 97, 64], H=2, G=4, page=32),
     "one query head": dict(new=[127, 128, 129, 257], past=[0, 5, 130, 260], H=2, G=1, page=256, groups=[0, 4], mem=[129]),
@@ -334,9 +335,18 @@ MANY_ROWS = {
 }
 
 
+def _wide(case):
+    """The case with enough (sequence, layer, key head) units for one kernel over memory and pages."""
+    if "groups" not in case:
+        return case
+    L = max(case.get("L", 1), -(-148 // (16 * len(case["new"]))))
+    mem = [(m if isinstance(m, list) else [m] * L) for m in case["mem"]]
+    return {**case, "H": 16, "L": L, "mem": [(m * L)[:L] for m in mem]}
+
+
 @pytest.mark.parametrize("name", list(BLOCKS) + list(MANY_ROWS))
 def test_attend_blocks_and_many_rows(name):
-    x = Batch(seed=21, **{**BLOCKS, **MANY_ROWS}[name])
+    x = Batch(seed=21, **(_wide(BLOCKS[name]) if name in BLOCKS else MANY_ROWS[name]))
     launches = x.call_attend(msa)
     assert launches == (1 if name in BLOCKS else 2)
     x.check()
@@ -356,7 +366,7 @@ def test_values_that_are_not_finite_in_many_blocks(G, new):
     for b, (page, slot) in enumerate(last):
         kept.append(x.pages[:, page, 1, :, slot].clone())
         x.pages[:, page, 1, :, slot, b % D] = float("inf") if b % 3 else float("nan")
-    x.call_attend(msa)
+    assert x.call_attend(msa) == 1
     got = x.out.clone()
     for b, (page, slot) in enumerate(last):
         x.pages[:, page, 1, :, slot] = kept[b]
@@ -375,8 +385,8 @@ def test_values_that_are_not_finite_in_many_blocks(G, new):
 
 
 def test_block_device_conditions():
-    x = Batch([40, 40, 40], [60, 60, 60], H=2, G=4, page=32, groups=[0, 3], mem=[50], seed=23)
-    x.call_attend(msa)
+    x = Batch([40, 40, 40], [60, 60, 60], L=4, H=16, G=4, page=32, groups=[0, 3], mem=[50], seed=23)
+    assert x.call_attend(msa) == 1
     good = x.out.clone()
     x.check()
     x.table[1, 1] = x.n_pages + 3               # rows 32..63 of sequence 1 are not seen
@@ -391,8 +401,8 @@ def test_block_device_conditions():
         keep = torch.tensor([r for r in range(61 + i) if not 32 <= r < 64], device="cuda")
         k = torch.cat([x.mem[0, 0, 0, :, :50].double(), loc[0, 0][:, keep]], 1)
         v = torch.cat([x.mem[0, 0, 1, :, :50].double(), loc[1, 0][:, keep]], 1)
-        s = torch.einsum("hgd,hkd->hgk", x.q[0, 40 + i].double().view(2, 4, D), k) * D ** -0.5
-        w = torch.einsum("hgk,hkd->hgd", torch.softmax(s, -1), v).reshape(8, D)
+        s = torch.einsum("hgd,hkd->hgk", x.q[0, 40 + i].double().view(16, 4, D), k) * D ** -0.5
+        w = torch.einsum("hgk,hkd->hgd", torch.softmax(s, -1), v).reshape(64, D)
         assert ((x.out[0, 40 + i].double() - w).abs() <= tol[0, 40 + i] + 2 ** -7 * w.abs()).all()
     x.err.zero_()
     x.mem_len[0, 0] = 50
@@ -476,3 +486,32 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     for x, want in zip(xs, alone):
         assert torch.equal(x.out.view(torch.int16), want.view(torch.int16)) and x.err.item() == 0
+
+
+@pytest.mark.parametrize("G,new", [(4, 20), (1, 100), (8, 33), (2, 64)])
+def test_one_row_tile_over_keys_of_all_lengths(G, new):
+    # sequences of one row tile: no key tile, one, two, odd and even numbers of them; one sequence
+    # with values that are not finite
+    past = [0, 100, 128 - new, 129, 300, 513, 40, 700, 1, 255]
+    x = Batch([new] * 10, [max(0, p) for p in past], L=2, H=8, G=G, page=16, groups=[0, 3, 6, 10], mem=[0, 128, 200],
+              seed=31)
+    x.seq_len[0] = 0  # (its rows see nothing)
+    assert x.call_attend(msa) == 1
+    x.check()
+    first = x.out.clone()
+    last = x.ids[5][(513 + new - 1) // 16], (513 + new - 1) % 16
+    x.pages[:, last[0], 1, :, last[1], 7] = float("-inf")
+    x.call_attend(msa)
+    end = 6 * new - 1
+    rest = torch.ones(x.T, dtype=torch.bool, device="cuda")
+    rest[end] = False
+    assert torch.equal(first[:, rest].view(torch.int16), x.out[:, rest].view(torch.int16))
+    assert (x.out[:, end, :, 7] == float("-inf")).all()
+    assert torch.equal(first[:, end, :, 8:].view(torch.int16), x.out[:, end, :, 8:].view(torch.int16))
+
+
+def test_few_sequences_over_a_long_memory_are_cut():
+    # blocks of new tokens, but too few for the GPU: the memory form, which cuts the memory
+    x = Batch([60, 90], [10, 70], H=2, G=4, groups=[0, 1, 2], mem=[3000, 1], seed=32)
+    assert x.call_attend(msa) == 2
+    x.check()

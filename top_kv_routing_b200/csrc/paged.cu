@@ -21,6 +21,7 @@ constexpr int kHalf = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSharedRows = 16;
 constexpr int kBlockRows = 64;
+constexpr int kBlockUnits = 148;
 constexpr int64_t kMaxTensorRows = 0x7fffffff - 128;  // (TMA row coordinates are 32-bit)
 
 // Which kernels a batch takes, by its average rows (tokens x G) per sequence and group (the
@@ -32,8 +33,9 @@ struct Plan {
 };
 Plan plan_of(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t Hq, int64_t H) {
   const int64_t G = Hq / H;
-  // Blocks of new tokens that fill half a row tile: memory and pages in one walk.
-  if (T * G >= kBlockRows * B) return {Plan::kBlocks, 0};
+  // Blocks of new tokens that fill half a row tile: memory and pages in one walk, if that makes a
+  // unit for every SM (it does not cut a unit's keys, the memory form does).
+  if (T * G >= kBlockRows * B && (NG == 0 || std::max(B, T * G / 256) * L * H >= kBlockUnits)) return {Plan::kBlocks, 0};
   // The memory once for a whole group, on the tensor cores, where its sequences share enough
   // rows; a group of one or two answers reads it sooner within the row kernel.
   if (NG > 0 && T * G > kSharedRows * NG) return {Plan::kMemory, memory_splits(L * T * Hq)};

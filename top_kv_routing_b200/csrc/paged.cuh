@@ -41,7 +41,8 @@ constexpr int kRowWorkers = kRowCtas * kRowWarps;
 // two piece slots per worker.
 constexpr size_t kWsCounters = 0;
 constexpr size_t kWsSplits = kRowWorkers * sizeof(int32_t);  // key splits that the memory kernel chose
-constexpr size_t kWsStat = kWsSplits + 128;
+constexpr size_t kWsOrder = kWsSplits + 128;  // the sequences in the block form's order
+constexpr size_t kWsStat = kWsOrder + kMaxSeqs * sizeof(int32_t);
 constexpr size_t kWsPart = kWsStat + (size_t)2 * kRowWorkers * 16 * sizeof(float2);
 constexpr size_t kWsEnd = kWsPart + (size_t)2 * kRowWorkers * 16 * kD * sizeof(float);
 

@@ -283,14 +283,41 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     ok_here &= s >= 0 && e >= s && e <= a.B;
   }
   auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
+  int32_t* order = reinterpret_cast<int32_t*>(a.ws + kWsOrder);  // (every CTA writes the same)
+  if (BLOCK) {
+    // the sequences by their keys, the most first (in the place of the tiles, not needed yet)
+    int* size = reinterpret_cast<int*>(smem + kOffRing);
+    for (int e = tid; e < a.B; e += kThreadsTc) {
+      const int len = a.seq_len[e];
+      int lo, n, from = 0, to = a.NG;  // the group: from <= it < to (whatever the offsets hold)
+      if (!sequence_tokens(a.q_offsets, e, a.T, lo, n) && blockIdx.x == 0)
+        msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+      if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
+      while (to - from > 1) {
+        const int mid = (from + to) >> 1;
+        if (a.group_offsets[mid] <= e) from = mid; else to = mid;
+      }
+      int keys = (int)min((int64_t)max(len, 0), cap) / kTile;
+      if (a.NG > 0 && a.group_offsets[from] <= e && e < a.group_offsets[from + 1])
+        keys += max(0, min(a.M_max, a.mem_len[(int64_t)from * a.L])) / kTile;
+      size[e] = n > 0 ? keys : -1;
+    }
+    __syncthreads();
+    for (int e = tid; e < a.B; e += kThreadsTc) {
+      const int own = size[e];
+      int rank = 0;
+      for (int f = 0; f < a.B; ++f) rank += size[f] > own || (size[f] == own && f < e);
+      order[rank] = e;
+    }
+    fence_async_smem();  // (the tiles come through the async proxy)
+    __syncthreads();
+  }
   for (int k = warp; k < n_blocks; k += kWarpsTc) {
     const int e = 32 * k + lane;
     int lo = 0, n = 0;
     if (e < n_entries) {
       if (BLOCK) {
-        if (!sequence_tokens(a.q_offsets, e, a.T, lo, n) && blockIdx.x == 0)
-          msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-        if (blockIdx.x == 0 && n > 0 && a.seq_len[e] > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
+        sequence_tokens(a.q_offsets, order[e], a.T, lo, n);
       } else {
         const int s = a.group_offsets[e], f = a.group_offsets[e + 1];
         if (s >= 0 && f >= s && f <= a.B) group_tokens(a, e, lo, n);
@@ -309,9 +336,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   const bool groups_ok = __syncthreads_and(ok_here);  // (where they are not, no group has a unit)
   tc_fence_after();
   if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-  // tokens of entry e; false where they are unusable
+  // tokens of entry e (block form: the e-th sequence in order); false where they are unusable
   auto entry_tokens = [&](int e, int& lo, int& n) -> bool {
-    if (BLOCK) return sequence_tokens(a.q_offsets, e, a.T, lo, n);
+    if (BLOCK) return sequence_tokens(a.q_offsets, order[e], a.T, lo, n);
     lo = n = 0;
     return groups_ok && group_tokens(a, e, lo, n);
   };
@@ -359,13 +386,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   const uint32_t tmem_base = tb.tmem;
   const int64_t n_units = (int64_t)pairs * LH * splits;
 
+  // Unit un of this CTA: in the block form every other round over the CTAs goes backwards, so that
+  // units which get smaller along the line even out.
+  auto unit_number = [&](int un) -> int64_t {
+    return (int64_t)un * gridDim.x + (BLOCK && (un & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  };
   // the unit (the lanes of one warp together)
   auto unit_at = [&](int64_t u) -> Unit {
     Unit x;
     // memory form: pairs run fastest (CTAs at work together read the same keys); block form:
-    // (layer, key head) runs fastest, and the sequences' last pairs, which see the most, first
+    // (layer, key head) runs fastest, then the pairs of a sequence
     const int64_t rest = BLOCK ? u / LH : u / pairs;
-    const int pair = BLOCK ? pairs - 1 - (int)rest : (int)(u - rest * pairs);
+    const int pair = BLOCK ? (int)rest : (int)(u - rest * pairs);
     const int s = BLOCK ? 0 : (int)(rest % splits);
     const int lh = BLOCK ? (int)(u - rest * LH) : (int)(rest / splits);
     x.l = lh / a.H;
@@ -384,7 +416,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
     before += tb.scan[k] - own_pairs;
     const int from = 31 - __clz(__ballot_sync(0xffffffffu, e < n_entries && before <= pair));
-    x.e = 32 * k + from;
+    x.e = BLOCK ? order[32 * k + from] : 32 * k + from;
     lo = __shfl_sync(0xffffffffu, lo, from);
     n = __shfl_sync(0xffffffffu, n, from);
     const int at = (pair - __shfl_sync(0xffffffffu, before, from)) * 2 * kTok;
@@ -525,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       __syncwarp();
     };
     int un = 0;
-    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
+    for (; unit_number(un) < n_units && ok; ++un) {
       if (!__all_sync(0xffffffffu, unit_wait(un))) {
         ok = false;
         break;
@@ -642,8 +674,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     uint32_t sn = 0, on = 0;  // score tiles and units so far
     uint32_t tiles = 0;       // key tiles of the pairs before (block form)
     bool ok = true;
-    int64_t u = blockIdx.x;
-    for (int un = 0; u < n_units && ok; u += gridDim.x, ++un) {
+    for (int un = 0; unit_number(un) < n_units && ok; ++un) {
       if (!__all_sync(0xffffffffu, unit_wait(un))) {
         ok = false;
         break;
@@ -865,7 +896,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       ++it;
     };
     int un = 0;
-    for (int64_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++un) {
+    for (; unit_number(un) < n_units && ok; ++un) {
       if (!__all_sync(0xffffffffu, unit_wait(un))) {
         ok = false;
         break;
@@ -931,8 +962,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       __syncwarp();
     };
-    int64_t u = blockIdx.x;
-    for (int un = 0; ok; u += gridDim.x, ++un) {
+    for (int un = 0; ok; ++un) {
+      const int64_t u = unit_number(un);
       if (u < n_units) {
         const Unit x = unit_at(u);
         if (!wait(&u_empty[un % kUnits], ((un / kUnits) & 1u) ^ 1u)) break;
