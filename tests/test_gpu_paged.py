@@ -306,8 +306,7 @@ def test_agrees_with_the_single_query_decode_step():
 # ----------------------------------------------------------------------------- long blocks, many rows
 
 BLOCKS = {
-    # rows per sequence (new x G) from 64 on walk memory and pages in one kernel, where that makes
-    # enough units for the GPU (the test adds key heads and layers until it does)
+    # long blocks of new tokens: memory and pages in one walk
     "one short block": dict(new=[16], past=[0], H=1, G=4),
     "edges of a tile pair": dict(new=[31, 32, 33, 63, 64, 65], past=[0, 127, 128, 1, 97, 64], H=2, G=4, page=32),
     "one query head": dict(new=[127, 128, 129, 257], past=[0, 5, 130, 260], H=2, G=1, page=256, groups=[0, 4], mem=[129]),
@@ -336,17 +335,15 @@ MANY_ROWS = {
 
 
 def _wide(case):
-    """The case with enough (sequence, layer, key head) units for one kernel over memory and pages."""
-    if "groups" not in case:
-        return case
-    L = max(case.get("L", 1), -(-148 // (16 * len(case["new"]))))
-    mem = [(m if isinstance(m, list) else [m] * L) for m in case["mem"]]
-    return {**case, "H": 16, "L": L, "mem": [(m * L)[:L] for m in mem]}
+    """The case with key heads and layers enough that the tensor-core kernels are taken."""
+    L = 8
+    mem = [(m if isinstance(m, list) else [m]) for m in case.get("mem", [])]
+    return {**case, "H": 16, "L": L, "mem": [(m * L)[:L] for m in mem] or None}
 
 
 @pytest.mark.parametrize("name", list(BLOCKS) + list(MANY_ROWS))
 def test_attend_blocks_and_many_rows(name):
-    x = Batch(seed=21, **(_wide(BLOCKS[name]) if name in BLOCKS else MANY_ROWS[name]))
+    x = Batch(seed=21, **_wide({**BLOCKS, **MANY_ROWS}[name]))
     launches = x.call_attend(msa)
     assert launches == (1 if name in BLOCKS else 2)
     x.check()
@@ -359,7 +356,7 @@ def test_attend_blocks_and_many_rows(name):
 @pytest.mark.parametrize("G,new", [(4, 70), (2, 140), (8, 33)])
 def test_values_that_are_not_finite_in_many_blocks(G, new):
     # several units per SM, every one with rows that must not see the last token's values
-    B, H = 24, 4
+    B, H = 24, 16
     x = Batch([new] * B, [(37 * b) % 150 for b in range(B)], L=2, H=H, G=G, page=32, groups=[0, B], mem=[130], seed=22)
     last = [(x.ids[b][(p + new - 1) // 32], (p + new - 1) % 32) for b, p in enumerate(x.past)]
     kept = []
@@ -385,7 +382,7 @@ def test_values_that_are_not_finite_in_many_blocks(G, new):
 
 
 def test_block_device_conditions():
-    x = Batch([40, 40, 40], [60, 60, 60], L=4, H=16, G=4, page=32, groups=[0, 3], mem=[50], seed=23)
+    x = Batch([40, 40, 40], [60, 60, 60], L=8, H=16, G=4, page=32, groups=[0, 3], mem=[50], seed=23)
     assert x.call_attend(msa) == 1
     good = x.out.clone()
     x.check()
@@ -445,8 +442,8 @@ def test_append_of_many_tokens_and_layers(dtype, with_q):
 
 def test_calls_follow_the_current_stream():
     # captured from the current stream, without a stream argument: append, block form and memory form
-    x = Batch([70, 60], [0, 20], H=2, G=4, groups=[0, 2], mem=[100], seed=26)
-    y = Batch([1] * 12, [30] * 12, H=2, G=4, groups=[0, 12], mem=[100], seed=27)
+    x = Batch([70, 60], [0, 20], L=8, H=16, G=4, groups=[0, 2], mem=[100], seed=26)
+    y = Batch([1] * 40, [30] * 40, L=8, H=16, G=4, groups=[0, 40], mem=[300], seed=27)
     for z in (x, y):
         z.call_attend(msa)
     q_rot = [torch.empty_like(z.out) for z in (x, y)]
@@ -472,11 +469,10 @@ def test_calls_follow_the_current_stream():
 
 
 def test_two_streams_with_their_own_workspaces():
-    xs = [Batch([1] * 40, [25] * 40, L=2, H=4, G=4, groups=[0, 40], mem=[900], seed=28),
-          Batch([50] * 6, [40] * 6, L=2, H=4, G=4, groups=[0, 6], mem=[500], seed=29),
+    xs = [Batch([1] * 40, [25] * 40, L=4, H=16, G=4, groups=[0, 40], mem=[900], seed=28),
+          Batch([50] * 6, [40] * 6, L=4, H=16, G=4, groups=[0, 6], mem=[500], seed=29),
           Batch([1] * 9, [700] * 9, L=2, H=4, G=4, seed=30)]
-    for x in xs:
-        x.call_attend(msa)
+    assert [x.call_attend(msa) for x in xs] == [2, 1, 1]
     torch.cuda.synchronize()
     alone = [x.out.clone() for x in xs]
     streams = [torch.cuda.Stream() for _ in xs]
@@ -493,7 +489,7 @@ def test_one_row_tile_over_keys_of_all_lengths(G, new):
     # sequences of one row tile: no key tile, one, two, odd and even numbers of them; one sequence
     # with values that are not finite
     past = [0, 100, 128 - new, 129, 300, 513, 40, 700, 1, 255]
-    x = Batch([new] * 10, [max(0, p) for p in past], L=2, H=8, G=G, page=16, groups=[0, 3, 6, 10], mem=[0, 128, 200],
+    x = Batch([new] * 10, [max(0, p) for p in past], L=4, H=16, G=G, page=16, groups=[0, 3, 6, 10], mem=[0, 128, 200],
               seed=31)
     x.seq_len[0] = 0  # (its rows see nothing)
     assert x.call_attend(msa) == 1
@@ -512,6 +508,6 @@ def test_one_row_tile_over_keys_of_all_lengths(G, new):
 
 def test_few_sequences_over_a_long_memory_are_cut():
     # blocks of new tokens, but too few for the GPU: the memory form, which cuts the memory
-    x = Batch([60, 90], [10, 70], H=2, G=4, groups=[0, 1, 2], mem=[3000, 1], seed=32)
+    x = Batch([60, 90], [10, 70], H=8, G=4, groups=[0, 1, 2], mem=[9000, 1], seed=32)
     assert x.call_attend(msa) == 2
     x.check()

@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "msa_paged.h"
@@ -19,27 +20,51 @@ using namespace paged;
 
 constexpr int kHalf = 64;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kSharedRows = 16;
-constexpr int kBlockRows = 64;
-constexpr int kBlockUnits = 148;
 constexpr int64_t kMaxTensorRows = 0x7fffffff - 128;  // (TMA row coordinates are 32-bit)
 
-// Which kernels a batch takes, by its average rows (tokens x G) per sequence and group (the
-// split of the tokens over the sequences is known to the device alone; any split is computed
-// correctly by every form).
+// Which kernels a batch takes (the split of the tokens over the sequences is known to the device
+// alone; any split is computed correctly by every form):
+//   kRows    the row kernel walks memory and pages of 8 or 16 rows (tokens x G) of a sequence;
+//   kMemory  the memory once for all rows of a group, on the tensor cores, cut into pieces where
+//            there are few of them, then the row kernel over the pages;
+//   kBlocks  memory and pages of 256 rows of a sequence on the tensor cores.
 struct Plan {
-  enum Form { kRowsOnly, kMemory, kBlocks } form;
+  enum Form { kRows, kMemory, kBlocks } form;
   int splits;  // memory form: most key splits
 };
-Plan plan_of(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t Hq, int64_t H) {
-  const int64_t G = Hq / H;
-  // Blocks of new tokens that fill half a row tile: memory and pages in one walk, if that makes a
-  // unit for every SM (it does not cut a unit's keys, the memory form does).
-  if (T * G >= kBlockRows * B && (NG == 0 || std::max(B, T * G / 256) * L * H >= kBlockUnits)) return {Plan::kBlocks, 0};
-  // The memory once for a whole group, on the tensor cores, where its sequences share enough
-  // rows; a group of one or two answers reads it sooner within the row kernel.
-  if (NG > 0 && T * G > kSharedRows * NG) return {Plan::kMemory, memory_splits(L * T * Hq)};
-  return {Plan::kRowsOnly, 0};
+
+// Whether a batch may take the memory form (its workspace follows from the sizes alone): groups
+// of more than eight rows, in short blocks or in few units.
+bool memory_form_open(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t G, int64_t H) {
+  return NG > 0 && T * G > 8 * NG && (T * G < 64 * B || std::max(B, T * G / 256) * L * H < 148);
+}
+
+// The form that takes least, estimated in cycles of a B200's 148 SMs from measured ones: 220 per
+// (16 keys, row tile) of the row kernel with all warps at work, and six of them for a row tile's
+// own costs; 3,100 per 128 keys and 5,000 per unit of the tensor-core kernel; 15,000 for each
+// kernel to start and end.  Measured on both sides of its borders (us): 16 answers over 256 keys,
+// 18 layers: memory form 85, rows 105; 33 drafts of 20 rows over 1,000 + 500 keys, 4 layers:
+// memory 112, blocks 166; 83 sequences of 56 rows, 7 layers: blocks 190, memory 330; one token
+// over 256 + 320 keys, 18 layers: rows 19, memory 31.
+Plan plan_of(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t Hq, int64_t H, int64_t mem_rows, int64_t page_rows) {
+  const double G = (double)(Hq / H), rows = T * G, units = (double)L * H, sms = 148;
+  const double M = NG > 0 ? (double)mem_rows : 0., P = (double)page_rows;
+  const double start = 15000, tile = 3100, unit = 5000, row_tile = 220;
+  const double R = rows <= 8. * B ? 8 : 16, row_tiles = B * std::ceil(rows / B / R);
+  const double pairs = std::max((double)B, rows / 256);
+  auto rows_cost = [&](double keys) { return start + units * row_tiles * (keys / 16 + 6) * row_tile / sms; };
+  Plan best = {Plan::kRows, 0};
+  double cost = rows_cost(M + P);
+  if (memory_form_open(T, B, NG, L, Hq / H, H)) {
+    const double c = start + units * std::max((double)NG, rows / 256) * (std::ceil(M / 128) * tile + unit) / sms + rows_cost(P);
+    if (c < cost) {
+      cost = c;
+      best = {Plan::kMemory, memory_splits(L * T * Hq)};
+    }
+  }
+  const double waves = std::max(std::ceil(units * B / sms), units * pairs / sms);
+  if (start + waves * ((std::ceil(M / 128) + std::ceil(P / 128)) * tile + unit) < cost) best = {Plan::kBlocks, 0};
+  return best;
 }
 
 static thread_local int32_t g_launches = 0;
@@ -369,9 +394,9 @@ extern "C" msa_status msa_shared_attend_workspace_size(int32_t n_tokens, int32_t
   if (st == MSA_OK) st = check_batch(n_tokens, n_seqs, n_layers);
   if (st != MSA_OK) return st;
   if (n_groups < 0 || n_groups > n_seqs) return msa_fail(MSA_ERR_INVALID_ARG, "n_groups must be in [0, n_seqs]");
-  const Plan plan = plan_of(n_tokens, n_seqs, n_groups, n_layers, n_q_heads, n_kv_heads);
   const int64_t rows = (int64_t)n_layers * n_tokens * n_q_heads;
-  *bytes = kWsEnd + (plan.form == Plan::kMemory ? memory_bytes(rows, plan.splits) : 0);
+  const bool memory = memory_form_open(n_tokens, n_seqs, n_groups, n_layers, n_q_heads / n_kv_heads, n_kv_heads);
+  *bytes = kWsEnd + (memory ? memory_bytes(rows, memory_splits(rows)) : 0);
   return msa_ok();
 }
 
@@ -426,10 +451,11 @@ extern "C" msa_status msa_shared_attend(const void* q, const int32_t* q_offsets,
   a.ws = static_cast<unsigned char*>(workspace);
   a.dev_err = dev_err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const Plan plan = plan_of(n_tokens, n_seqs, n_groups, n_layers, n_q_heads, n_kv_heads);
+  const Plan plan = plan_of(n_tokens, n_seqs, n_groups, n_layers, n_q_heads, n_kv_heads, a.M_max,
+                            (int64_t)max_pages * page_size);
   const int64_t mem_rows = (int64_t)n_groups * n_layers * 2 * n_kv_heads * a.M_max;
   const int64_t page_rows = ((int64_t)n_layers * n_pages * 2 * n_kv_heads) << a.log2_page;
-  if (plan.form != Plan::kRowsOnly && (mem_rows > kMaxTensorRows || (plan.form == Plan::kBlocks && page_rows > kMaxTensorRows)))
+  if (plan.form != Plan::kRows && (mem_rows > kMaxTensorRows || (plan.form == Plan::kBlocks && page_rows > kMaxTensorRows)))
     return msa_fail(MSA_ERR_CAPACITY, "mem_kv or kv_pages beyond 2^31 rows of 128 elements");
   if (plan.form == Plan::kBlocks) {
     MSA_CUDA_TRY(launch_blocks(a, s));

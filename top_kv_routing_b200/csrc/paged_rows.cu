@@ -537,88 +537,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           o[n][1] += o[n][3];
         }
       }
-      bool write = true;
-      const int64_t u1 = u0 + c.nt;
-      if (u0 < w0 || u1 > w1) {
-        // a cut unit: pieces belong to workers first .. last; the piece at a worker's start
-        // (a unit begun before it) goes to slot 2 w, the one it begins to slot 2 w + 1
-        const int first = (int)divide(u0, per), last = (int)divide(u1 - 1, per);
-        float2* stat = reinterpret_cast<float2*>(a.ws + kWsStat);
-        float* part = reinterpret_cast<float*>(a.ws + kWsPart);
-        int* counter = reinterpret_cast<int*>(a.ws + kWsCounters) + first;
-        const int64_t slot = 2 * (int64_t)worker + (u0 < w0 ? 0 : 1);
-#pragma unroll
-        for (int v = 0; v < NR; ++v) {
-          const int r = g + 8 * v;
-          if (row_token(r) < tb.n[c.b]) {
-            float* dst = part + (slot * 16 + r) * kD + 2 * t;
-#pragma unroll
-            for (int n = 0; n < 16; ++n)
-              __stcg(reinterpret_cast<float2*>(dst + 8 * n), make_float2(o[n][2 * v], o[n][2 * v + 1]));
-            if (t == 0) __stcg(&stat[slot * 16 + r], make_float2(m[v], sum[v]));
-          }
-        }
-        __threadfence();
-        __syncwarp();
-        int old = 0;
-        if (lane == 0) old = atomicAdd(counter, 1);
-        old = __shfl_sync(0xffffffffu, old, 0);
-        write = old == last - first;
-        if (write) {
-          __threadfence();
-          if (lane == 0) *counter = 0;  // ready for the next call
-#pragma unroll
-          for (int v = 0; v < NR; ++v) {
-            const int r = g + 8 * v;
-            m[v] = -INFINITY;
-            sum[v] = 0.f;
-#pragma unroll
-            for (int n = 0; n < 16; ++n) o[n][2 * v] = o[n][2 * v + 1] = 0.f;
-            if (row_token(r) < tb.n[c.b]) {
-              for (int w = first; w <= last; ++w) m[v] = fmaxf(m[v], __ldcg(&stat[(2 * w + (w == first)) * 16 + r]).x);
-              const float base = m[v] == -INFINITY ? 0.f : m[v];
-              for (int w = first; w <= last; ++w) {
-                const int64_t sl = 2 * (int64_t)w + (w == first);
-                const float2 ml = __ldcg(&stat[sl * 16 + r]);
-                const float f = ex2_ftz(ml.x - base);
-                sum[v] = fmaf(f, ml.y, sum[v]);
-                const float* src = part + (sl * 16 + r) * kD + 2 * t;
-#pragma unroll
-                for (int n = 0; n < 16; ++n) {
-                  const float2 x = __ldcg(reinterpret_cast<const float2*>(src + 8 * n));
-                  o[n][2 * v] = fmaf(f, x.x, o[n][2 * v]);
-                  o[n][2 * v + 1] = fmaf(f, x.y, o[n][2 * v + 1]);
-                }
-              }
-            }
-          }
-        }
-      }
-      if (PART && write && tb.grp[c.b] >= 0) {
-        // join the memory part: its slots in order, then this sequence's rows
-        if (!memory_done) {
-          wait_for_earlier_kernels();
-          memory_done = true;
-        }
-        const int slots = __ldcg(reinterpret_cast<const int*>(a.ws + kWsSplits)) * tb.gmt[tb.grp[c.b]];
-        const int64_t all_rows = (int64_t)a.L * a.T * Hq;
-        const float* part = reinterpret_cast<const float*>(a.ws + kWsMemory);
-        const float2* stat =
-            reinterpret_cast<const float2*>(a.ws + kWsMemory + memory_part_bytes(all_rows, max_splits));
-        // With fewer than eight rows several of the eight quads of lanes share a row: of its
-        // `share` quads, number `mine` takes the slots mine, mine + share, ...
-        const int valid = min(kTok, tb.n[c.b] - c.rt * kTok) * G;
-        const int vr = valid > 4 ? 8 : valid > 2 ? 4 : valid;
-        const int share = 8 / vr, mine = g / vr;
+      // Joins `n` partial results (place(i, r): of row r the i-th one's index) to what the rows
+      // hold.  With fewer than eight rows several of the eight quads of lanes share a row: of its
+      // `share` quads, number `mine` takes the places mine, mine + share, ...
+      const int valid = min(kTok, tb.n[c.b] - c.rt * kTok) * G;
+      const int vr = valid > 4 ? 8 : valid > 2 ? 4 : valid;
+      const int share = 8 / vr, mine = g / vr;
+      auto join = [&](int n_places, const float2* stat, const float* part, auto place) {
 #pragma unroll
         for (int v = 0; v < NR; ++v) {
           if (v > 0 && valid <= 8) break;
           const int r = (g & (vr - 1)) + 8 * v;
-          const bool has = r < valid;
-          const int64_t row = has ? row_at(r) / kD : 0;
-          const int n_slots = has ? slots : 0;
+          const int n_mine = r < valid ? n_places : 0;
           float top = __shfl_sync(0xffffffffu, m[v], ((g & (vr - 1)) << 2) | t);
-          for (int s = mine * 4 + t; s < n_slots; s += 4 * share) top = fmaxf(top, __ldcg(&stat[s * all_rows + row]).x);
+          for (int s = mine * 4 + t; s < n_mine; s += 4 * share) top = fmaxf(top, __ldcg(&stat[place(s, r)]).x);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           for (int o2 = 4 * vr; o2 < 32; o2 <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
@@ -630,16 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[n][2 * v] = mine == 0 ? o[n][2 * v] * own : 0.f;
             o[n][2 * v + 1] = mine == 0 ? o[n][2 * v + 1] * own : 0.f;
           }
-          const float* src = part + row * kD + 4 * t;
+          m[v] = top;
 #pragma unroll 2
-          for (int s = mine; s < n_slots; s += share) {
-            const float2 ml = __ldcg(&stat[s * all_rows + row]);
-            const bool use = ml.y != 0.f;  // (an empty split writes no output)
+          for (int s = mine; s < n_mine; s += share) {
+            const int64_t at_s = place(s, r);
+            const float2 ml = __ldcg(&stat[at_s]);
+            const bool use = ml.y != 0.f;  // (where no key was seen the output may not be written)
             const float f = use ? ex2_ftz(ml.x - base) : 0.f;
             float4 x[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              x[k] = use ? __ldcg(reinterpret_cast<const float4*>(src + s * all_rows * kD + 16 * k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              x[k] = use ? __ldcg(reinterpret_cast<const float4*>(part + at_s * kD + 16 * k + 4 * t)) : make_float4(0.f, 0.f, 0.f, 0.f);
             sum[v] = fmaf(f, ml.y, sum[v]);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -658,6 +591,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+      };
+      bool write = true;
+      const int64_t u1 = u0 + c.nt;
+      if (u0 < w0 || u1 > w1) {
+        // a cut unit: pieces belong to workers first .. last; the piece at a worker's start
+        // (a unit begun before it) goes to slot 2 w, the one it begins to slot 2 w + 1
+        const int first = (int)divide(u0, per), last = (int)divide(u1 - 1, per);
+        float2* stat = reinterpret_cast<float2*>(a.ws + kWsStat);
+        float* part = reinterpret_cast<float*>(a.ws + kWsPart);
+        int* counter = reinterpret_cast<int*>(a.ws + kWsCounters) + first;
+        const int64_t slot = 2 * (int64_t)worker + (u0 < w0 ? 0 : 1);
+#pragma unroll
+        for (int v = 0; v < NR; ++v) {
+          const int r = g + 8 * v;
+          if (r < valid) {
+            float* dst = part + (slot * 16 + r) * kD + 4 * t;  // (the order that `join` reads)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              __stcg(reinterpret_cast<float4*>(dst + 16 * k),
+                     make_float4(o[2 * k][2 * v], o[2 * k][2 * v + 1], o[2 * k + 1][2 * v], o[2 * k + 1][2 * v + 1]));
+            if (t == 0) __stcg(&stat[slot * 16 + r], make_float2(m[v], sum[v]));
+          }
+        }
+        __threadfence();
+        __syncwarp();
+        int old = 0;
+        if (lane == 0) old = atomicAdd(counter, 1);
+        old = __shfl_sync(0xffffffffu, old, 0);
+        write = old == last - first;
+        if (write) {
+          __threadfence();
+          if (lane == 0) *counter = 0;  // ready for the next call
+#pragma unroll
+          for (int v = 0; v < NR; ++v) {
+            m[v] = -INFINITY;
+            sum[v] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 16; ++n) o[n][2 * v] = o[n][2 * v + 1] = 0.f;
+          }
+          join(last - first + 1, stat, part, [&](int i, int r) -> int64_t { return (2 * (int64_t)(first + i) + (i == 0)) * 16 + r; });
+        }
+      }
+      if (PART && write && tb.grp[c.b] >= 0) {
+        // join the memory part: its slots in order, then this sequence's rows
+        if (!memory_done) {
+          wait_for_earlier_kernels();
+          memory_done = true;
+        }
+        const int slots = __ldcg(reinterpret_cast<const int*>(a.ws + kWsSplits)) * tb.gmt[tb.grp[c.b]];
+        const int64_t all_rows = (int64_t)a.L * a.T * Hq;
+        join(slots, reinterpret_cast<const float2*>(a.ws + kWsMemory + memory_part_bytes(all_rows, max_splits)),
+             reinterpret_cast<const float*>(a.ws + kWsMemory),
+             [&](int s, int r) -> int64_t { return s * all_rows + row_at(r) / kD; });
       }
       if (write) {
 #pragma unroll
