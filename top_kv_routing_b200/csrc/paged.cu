@@ -1,5 +1,5 @@
-// Paged batches: the append kernel and the entry points (the attention kernels are in
-// paged_rows.cu).
+// Paged batches: the append kernel, the choice of the attention kernels and the entry points (those
+// kernels are in paged_rows.cu and paged_tc.cu).
 //
 // Follows "MSA端到端可训练记忆模型完整开源，支持亿级Token上下文", section 架构 (全局 RoPE: positions
 // offset by k; local K/V joined to the selected memory), and the MSA paper reading notes,
@@ -99,7 +99,7 @@ const RopeFreq& rope_freq(float theta) {
 // The first rows are loaded before the position is known and the next before the ones at hand are
 // stored.  Bound by HBM: every byte moves once.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendCtas = 148 * 8;  // runs of layers are as long as leaves so many CTAs
+constexpr int kAppendCtas = 148 * 7;  // runs of layers are as long as leaves so many CTAs (five fit an SM)
 
 struct AppendArgs {
   const void *q, *k, *v;
@@ -161,6 +161,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   __shared__ int s_own;      // the token belongs to a sequence
   const int t = blockIdx.x, l0 = blockIdx.y * a.run, nl = min(a.run, a.L - l0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (what the search below reads one after the other: asked of L2 at once)
+  prefetch_line(a.off, (a.B + 1) * 4ll, tid);
+  prefetch_line(a.seq_len, a.B * 4ll, tid);
+  if (a.pos_offset) prefetch_line(a.pos_offset, a.B * 4ll, tid);
+  prefetch_line(a.table, (int64_t)a.B * a.max_pages * 4, tid);
   wait_for_earlier_kernels();
   let_next_kernel_start();
   const int p = tid & 7;  // dims 8p .. 8p + 7 and 64 + 8p .. (kAppendThreads is a multiple of 8)

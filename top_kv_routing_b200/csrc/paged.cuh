@@ -100,6 +100,12 @@ __device__ __forceinline__ void let_next_kernel_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Asks L2 for the i-th 128 bytes of an array (no value is read, so it may run ahead of earlier
+// kernels).
+__device__ __forceinline__ void prefetch_line(const void* p, int64_t bytes, int64_t i) {
+  if (i * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + i * 128));
+}
+
 // The tokens [lo, lo + n) of sequence b; n = 0 and false where the offsets are unusable.
 __device__ __forceinline__ bool sequence_tokens(const int32_t* __restrict__ off, int b, int T, int& lo, int& n) {
   lo = off[b];

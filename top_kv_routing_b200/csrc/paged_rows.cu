@@ -11,7 +11,8 @@
 // in the order (sequence, layer, key head, row tile, key tile), form one line that is cut
 // into equal pieces, one per warp of the grid (one 8-warp CTA per SM), so that ragged lengths
 // do not leave SMs idle and a single long sequence is spread over all of them.  A unit takes
-// six tiles more on the line than it has (its queries, join and output cost about that).
+// six tiles more on the line than it has (its queries, join and output cost about that; nine where
+// the memory kernel's results are joined too).
 //
 // Each warp streams its tiles through its own 3-stage cp.async ring in shared memory (16 K
 // rows and 16 V rows a stage, 16-byte chunks XOR-swizzled by row so ldmatrix is
@@ -43,7 +44,6 @@ constexpr int kStageBytes = 2 * kTileKeys * kRowBytes;  // 16 K rows, then 16 V 
 constexpr int kRingBytes = kRowWarps * kStages * kStageBytes;
 constexpr int kMinTiles = 2;  // tiles per warp below which a unit is not cut further
 constexpr float kHeadroom = 8.0f; // log2 growth of a row's maximum tolerated before rescaling
-constexpr int kUnitTicks = 6; // what a unit costs beyond its tiles (queries in, join, output), in tiles
 
 // The tables of the batch in shared memory.
 struct Tables {
@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     rows_kernel(const __grid_constant__ Attend a, int max_splits) {
   constexpr int R = 8 * NR;       // rows of a unit
   constexpr int kTok = R / G;     // tokens of a unit
+  constexpr int kUnitTicks = PART ? 9 : 6;  // what a unit costs beyond its tiles (queries in, joins, output), in tiles
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Tables& tb = *reinterpret_cast<Tables*>(smem_raw + kRingBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
