@@ -99,13 +99,15 @@ class Batch:
                 return g
         return None
 
-    def attend(self, scale=D ** -0.5):
+    def attend(self, scale=D ** -0.5, only=None):
         """(expected output, tolerance), both [L, T, HQ, D] fp64; tolerance < 0 where the output
-        is to be left as it was."""
+        is to be left as it was (and for sequences not in `only`)."""
         L, H, G = self.L, self.H, self.G
         want = torch.zeros((L, self.T, self.HQ, D), dtype=torch.float64, device=self.q.device)
         tol = torch.full_like(want, -1.0)
         for b, (new, past) in enumerate(zip(self.new, self.past)):
+            if only is not None and b not in only:
+                continue
             t0 = self.off[b].item()
             ln = self.seq_len[b].item()
             cut = ln - new

@@ -511,3 +511,17 @@ def test_few_sequences_over_a_long_memory_are_cut():
     x = Batch([60, 90], [10, 70], H=8, G=4, groups=[0, 1, 2], mem=[9000, 1], seed=32)
     assert x.call_attend(msa) == 2
     x.check()
+
+
+@pytest.mark.parametrize("B", [511, 513])
+def test_blocks_of_many_sequences(B):
+    # both sides of the number of sequences that are put in order
+    new = [17 + b % 3 for b in range(B)]
+    x = Batch(new, [(11 * b) % 29 for b in range(B)], H=1, G=8, groups=[0, 5, B - 1], mem=[3, 20], seed=33)
+    x.call_attend(msa)
+    pick = [0, 4, 5, 77, B - 2, B - 1]
+    want, tol = x.attend(only=pick)
+    for b in pick:
+        at = slice(x.off[b].item(), x.off[b + 1].item())
+        assert ((x.out[:, at].double() - want[:, at]).abs() <= tol[:, at]).all()
+    assert not x.out.isnan().any() and x.err.item() == 0

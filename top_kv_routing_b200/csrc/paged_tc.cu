@@ -74,6 +74,7 @@ constexpr uint32_t kTmemCols = 512;       // S_a | S_b | O_a | O_b
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kHeadroom = 8.0f;         // log2 growth of a row's maximum tolerated before rescaling
 
+constexpr int kOrdered = 512;             // most sequences that are put in order
 constexpr int kBadRing = 8;               // tiles whose page masks are kept (more than are in flight)
 
 // One unit as every role sees it.
@@ -285,7 +286,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
   int32_t* order = reinterpret_cast<int32_t*>(a.ws + kWsOrder);  // (every CTA writes the same)
   if (BLOCK) {
-    // the sequences by their keys, the most first (in the place of the tiles, not needed yet)
+    // the sequences by their keys, the most first (in the place of the tiles, not needed yet);
+    // beyond kOrdered of them the comparisons would cost more than the order gives
     int* size = reinterpret_cast<int*>(smem + kOffRing);
     for (int e = tid; e < a.B; e += kThreadsTc) {
       const int len = a.seq_len[e];
@@ -305,8 +307,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     __syncthreads();
     for (int e = tid; e < a.B; e += kThreadsTc) {
       const int own = size[e];
-      int rank = 0;
-      for (int f = 0; f < a.B; ++f) rank += size[f] > own || (size[f] == own && f < e);
+      int rank = a.B > kOrdered ? e : 0;
+      for (int f = 0; f < a.B && a.B <= kOrdered; ++f) rank += size[f] > own || (size[f] == own && f < e);
       order[rank] = e;
     }
     fence_async_smem();  // (the tiles come through the async proxy)
