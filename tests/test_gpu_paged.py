@@ -323,7 +323,7 @@ BLOCKS = {
 
 MANY_ROWS = {
     # groups of more than one, two, four row tiles; the memory split over few and many units
-    "one tile": dict(new=[1] * 32, past=[i for i in range(32)], H=1, G=4, groups=[0, 32], mem=[129]),
+    "one tile": dict(new=[1] * 32, past=[i for i in range(32)], H=1, G=4, groups=[0, 32], mem=[401]),
     "a tile and a row": dict(new=[1] * 33, past=[2] * 33, H=1, G=4, groups=[0, 33], mem=[500]),
     "pairs of tiles": dict(new=[1] * 150, past=[i % 40 for i in range(150)], H=2, G=4, groups=[0, 150], mem=[300]),
     "groups of all sizes": dict(new=[1] * 100, past=[i % 23 for i in range(100)], L=2, H=2, G=8,

@@ -40,30 +40,34 @@ bool memory_form_open(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t G, in
 }
 
 // The form that takes least, estimated in cycles of a B200's 148 SMs from measured ones: 220 per
-// (16 keys, row tile) of the row kernel with all warps at work, and six of them for a row tile's
-// own costs; 3,100 per 128 keys and 5,000 per unit of the tensor-core kernel; 15,000 for each
-// kernel to start and end.  Measured on both sides of its borders (us): 16 answers over 256 keys,
-// 18 layers: memory form 85, rows 105; 33 drafts of 20 rows over 1,000 + 500 keys, 4 layers:
-// memory 112, blocks 166; 83 sequences of 56 rows, 7 layers: blocks 190, memory 330; one token
-// over 256 + 320 keys, 18 layers: rows 19, memory 31.
+// (16 keys, row tile) of the row kernel with all warps at work, six of them for a row tile's own
+// costs and ten where the memory's results are joined to it; 3,100 per 128 keys and 5,000 per unit
+// of the tensor-core kernel; 20,000 for each kernel of the first two forms to start and end, 15,000
+// for the third.  The lengths are the largest ones that the buffers allow.  Of 228 batches of all
+// sizes, timed in every form that they may take, 223 got a form within 12 % of the best, 1 % from
+// it on average.  Both sides of the borders (us): 16 answers over 256 + 320 keys, 18 layers: memory
+// 99, rows 94; 33 drafts of 20 rows over 1,000 + 500 keys, 4 layers: memory 124, rows 180, blocks
+// 176; 128 answers in 16 groups: memory 450, rows 840; 47 tokens of 40 sequences over 500 + 250
+// keys, 6 layers: blocks 158, memory 216, rows 268.
 Plan plan_of(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t Hq, int64_t H, int64_t mem_rows, int64_t page_rows) {
-  const double G = (double)(Hq / H), rows = T * G, units = (double)L * H, sms = 148;
+  const double G = (double)(Hq / H), rows = (double)T * G, units = (double)L * H, sms = 148;
   const double M = NG > 0 ? (double)mem_rows : 0., P = (double)page_rows;
-  const double start = 15000, tile = 3100, unit = 5000, row_tile = 220;
+  const double start = 20000, start_blocks = 15000, tile = 3100, unit = 5000, row_tile = 220;
   const double R = rows <= 8. * B ? 8 : 16, row_tiles = B * std::ceil(rows / B / R);
   const double pairs = std::max((double)B, rows / 256);
-  auto rows_cost = [&](double keys) { return start + units * row_tiles * (keys / 16 + 6) * row_tile / sms; };
+  auto rows_cost = [&](double keys, double own) { return start + units * row_tiles * (keys / 16 + own) * row_tile / sms; };
   Plan best = {Plan::kRows, 0};
-  double cost = rows_cost(M + P);
+  double cost = rows_cost(M + P, 6);
   if (memory_form_open(T, B, NG, L, Hq / H, H)) {
-    const double c = start + units * std::max((double)NG, rows / 256) * (std::ceil(M / 128) * tile + unit) / sms + rows_cost(P);
+    const double c =
+        start + units * std::max((double)NG, rows / 256) * (std::ceil(M / 128) * tile + unit) / sms + rows_cost(P, 10);
     if (c < cost) {
       cost = c;
       best = {Plan::kMemory, memory_splits(L * T * Hq)};
     }
   }
   const double waves = std::max(std::ceil(units * B / sms), units * pairs / sms);
-  if (start + waves * ((std::ceil(M / 128) + std::ceil(P / 128)) * tile + unit) < cost) best = {Plan::kBlocks, 0};
+  if (start_blocks + waves * ((std::ceil(M / 128) + std::ceil(P / 128)) * tile + unit) < cost) best = {Plan::kBlocks, 0};
   return best;
 }
 
