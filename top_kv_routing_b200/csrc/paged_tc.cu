@@ -43,7 +43,8 @@
 // S_x(j + 1) is issued after PV_x(j), so its completion also says that O_x is stable: the
 // softmax rescales it without another wait.  Key rows past the last valid one are zeroed in
 // shared memory before the PV that reads them (they may hold anything).  Every wait is
-// bounded (2 s); a timeout sets MSA_DEVERR_TIMEOUT and the CTA drains and frees its TMEM.
+// bounded (2 s, and 60 s where a wait may last a whole unit); a timeout sets MSA_DEVERR_TIMEOUT and
+// the CTA drains and frees its TMEM.
 #include <cuda.h>
 
 #include <algorithm>
@@ -74,6 +75,7 @@ constexpr uint32_t kTmemCols = 512;       // S_a | S_b | O_a | O_b
 constexpr uint32_t kColS = 0, kColO = 256;
 constexpr float kHeadroom = 8.0f;         // log2 growth of a row's maximum tolerated before rescaling
 
+constexpr unsigned long long kUnitWaitNs = 60000000000ull;  // (a failure within a unit is noticed by a shorter wait)
 constexpr int kOrdered = 512;             // most sequences that are put in order
 constexpr int kBadRing = 8;               // tiles whose page masks are kept (more than are in flight)
 
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     return (valid_keys(x, tile) & 15) != 0 || (BLOCK && tile >= x.mt && (tile - x.mt + 1) * kTile > x.lim0);
   };
   // unit un of this CTA (every lane of the caller's warp, or its one thread, waits)
-  auto unit_wait = [&](int un) -> bool { return mbar_wait(smem_u32(&u_full[un % kUnits]), (un / kUnits) & 1u, abort_flag); };
+  auto unit_wait = [&](int un) -> bool { return mbar_wait(smem_u32(&u_full[un % kUnits]), (un / kUnits) & 1u, abort_flag, kUnitWaitNs); };
 
   // (setmaxnreg in each role's own branch: the compiler allocates what follows by it)
   if (warp == kTmaWarp) {
@@ -693,7 +695,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       float m = -INFINITY;
       float sum = 0.f;
       for (int j = 0; j < n; ++j) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[st]), sn & 1u, abort_flag))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_ready[st]), sn & 1u, abort_flag, kUnitWaitNs))) {
           ok = false;
           break;
         }
@@ -948,7 +950,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     bool ok = true;
     uint32_t qn[2] = {0, 0};  // query tiles loaded per stream
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag))) ok = false;
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag, kUnitWaitNs))) ok = false;
       return ok;
     };
     auto load_q = [&](const Unit& x, int st) {
