@@ -45,6 +45,12 @@
 // shared memory before the PV that reads them (they may hold anything).  Every wait is
 // bounded (2 s, and 60 s where a wait may last a whole unit); a timeout sets MSA_DEVERR_TIMEOUT and
 // the CTA drains and frees its TMEM.
+//
+// Measured on one B200: 256 rows x 8 key heads x 16,384 keys of a wide batch (137 GFLOP) in 140 us,
+// the tensor pipe 63 % active, 128 units on 148 SMs; a tile pair takes 3,100 cycles against 2,048
+// of MMA, because a stream's softmax (1,024 cycles of exponentials on the MUFU alone), its PV and
+// its next scores follow one another and two outputs leave tensor memory no second score buffer.
+// Short units wait for instruction fetch: the softmax has one body and the other roles loops.
 #include <cuda.h>
 
 #include <algorithm>
