@@ -28,7 +28,7 @@
 // arrive (a counter that it resets) joins the pieces in their order along the line, so the
 // result does not depend on the order of arrival.
 //
-// Measured on one B200: 128 answers of 256 page rows on average, 18 layers, 32 / 8 heads: 2.0 GB of
+// Measured on one B200: 128 answers of 215 page rows on average, 18 layers, 32 / 8 heads: 2.0 GB of
 // pages in 345 us (5.9 TB/s, 0.9 of the copy rate); one token over 256 + 320 keys, 18 layers (42
 // MB): 18 us.  With many tiles a warp HBM bounds it; with few the chain of a launch does (tables,
 // page ids, first keys, joins), and otherwise the warps' own latencies: 420 instructions a tile at
