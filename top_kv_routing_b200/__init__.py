@@ -15,4 +15,6 @@ _SUBMODULES = {"abi", "build", "engine"}
 def __getattr__(name: str):
     if name.startswith("__") or name in _SUBMODULES:
         raise AttributeError(name)
-    return getattr(importlib.import_module(__name__ + ".abi"), name)
+    value = getattr(importlib.import_module(__name__ + ".abi"), name)
+    globals()[name] = value  # (found without this function from now on: it costs 1 us)
+    return value

@@ -147,9 +147,10 @@ def _ptr(t) -> int | None:
     """Raw address of a torch tensor / numpy array (None stays NULL)."""
     if t is None:
         return None
-    if isinstance(t, np.ndarray):
+    try:
+        return t.data_ptr()
+    except AttributeError:
         return t.ctypes.data
-    return t.data_ptr()
 
 
 def _nbytes(t) -> int:
