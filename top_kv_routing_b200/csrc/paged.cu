@@ -101,7 +101,7 @@ const RopeFreq& rope_freq(float theta) {
 // its page slot and the 64 angles of its position, once for all layers of the run; then eight
 // threads per head row rotate (query and key heads) or copy (value heads) 8 + 8 elements each.
 // The first rows are loaded before the position is known and the next before the ones at hand are
-// stored.  Bound by HBM: every byte moves once (2.7 GB of long texts in 422 us, 0.99 of the copy
+// stored.  Bound by HBM: every byte moves once (2.7 GB of long texts in 420 us, 0.99 of the copy
 // rate; one token 3.3 us in a graph).
 constexpr int kAppendThreads = 256;
 constexpr int kAppendCtas = 148 * 7;  // runs of layers are as long as leaves so many CTAs (five fit an SM)
