@@ -172,12 +172,19 @@ __device__ __forceinline__ void tma_load_rows(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// 32 bytes at a 16-byte boundary (all that `out` and the workspace have to keep: one store of 32
-// bytes would need a multiple of 32).
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&x)[8]) {
-  uint4* dst = static_cast<uint4*>(p);
-  dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
-  dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+// 32 bytes, in one store where the buffer they belong to starts at a multiple of 32 (all offsets
+// within it are), in two where it keeps only the 16 bytes that `out` and the workspace have to.
+// The wide stores take 298 us over the 18 layers of 8 questions, the others 318.
+__device__ __forceinline__ void st_global_32(void* p, bool wide, const uint32_t (&x)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    uint4* dst = static_cast<uint4*>(p);
+    dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
 }
 
 // Packed pairs of fp32 (two registers).
@@ -682,6 +689,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     float* part = reinterpret_cast<float*>(a.ws + kWsMemory);
     const int64_t all_rows = (int64_t)a.L * a.T * Hq;
     float2* stat = reinterpret_cast<float2*>(a.ws + kWsMemory + memory_part_bytes(all_rows, max_splits));
+    const bool wide = ((BLOCK ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(part)) & 31u) == 0;
     const f32x2 scale2 = pack2(a.qscale, a.qscale);
     uint32_t sn = 0, on = 0;  // score tiles and units so far
     uint32_t tiles = 0;       // key tiles of the pairs before (block form)
@@ -814,7 +822,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
 #pragma unroll
             for (int v = 0; v < 8; ++v)
               w[v] = msa::float2_to_bf16x2(__uint_as_float(o[16 * e + 2 * v]) * inv, __uint_as_float(o[16 * e + 2 * v + 1]) * inv);
-            st_global_32(dst + 16 * e, w);
+            st_global_32(dst + 16 * e, wide, w);
           }
         } else if (mine && n > 0) {
 #pragma unroll
@@ -822,7 +830,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             // (the row kernel's order: of every 16 dims, 0 1 8 9, 2 3 10 11, 4 5 12 13, 6 7 14 15)
             const int d = 16 * (e >> 1) + 4 * (e & 1);
             const uint32_t w[8] = {o[d], o[d + 1], o[d + 8], o[d + 9], o[d + 2], o[d + 3], o[d + 10], o[d + 11]};
-            st_global_32(part + row * kD + 32 * c + 8 * e, w);
+            st_global_32(part + row * kD + 32 * c + 8 * e, wide, w);
           }
         }
       }
