@@ -102,7 +102,8 @@ msa_status msa_shared_attend_workspace_size(int32_t n_tokens, int32_t n_seqs, in
  * past max_pages * page_size is clamped with MSA_DEVERR_LOCAL_FULL; rows of a page id outside
  * [0, n_pages) are not seen (MSA_DEVERR_BAD_PAGE); q_offsets or group_offsets that decrease or
  * leave their range set MSA_DEVERR_BAD_OFFSETS and such a sequence (its output left as it
- * was) or group (no memory) is skipped.  Waits inside the tensor-core kernel are bounded: a timeout
+ * was) or group (no memory) is skipped, no other; where that leaves a sequence in several groups,
+ * the last one's memory counts, and tokens in several sequences have undefined outputs.  Waits inside the tensor-core kernel are bounded: a timeout
  * sets MSA_DEVERR_TIMEOUT and leaves the output and the workspace undefined (zero it again).
  * Asynchronous on `stream`, graph-capturable, launched as programmatic dependents. */
 msa_status msa_shared_attend(const void* q, const int32_t* q_offsets, int32_t n_tokens, int32_t n_seqs,

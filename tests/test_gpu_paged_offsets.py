@@ -1,0 +1,84 @@
+"""Paged batches with unusable offsets: the sequences and groups that have them are skipped, all
+others get what include/msa_paged.h defines, in every form of the kernels."""
+import pytest
+import torch
+
+import top_kv_routing_b200 as msa
+from paged_ref import Batch, rope
+from test_gpu_paged_forms import forms
+
+pytestmark = pytest.mark.gpu
+
+
+def _check_only(x, good):
+    """Outputs of the sequences in `good` as defined, those of all others untouched."""
+    want, tol = x.attend(only=good)
+    own = torch.zeros(x.T, dtype=torch.bool, device="cuda")
+    for b in good:
+        at = slice(x.off[b].item(), x.off[b].item() + x.new[b])
+        own[at] = True
+        assert ((x.out[:, at].double() - want[:, at]).abs() <= tol[:, at]).all(), b
+    assert (x.out[:, ~own] == 7.0).all()
+
+
+# batches of 40 sequences in three groups, one for each form: few rows a group; memory once for all
+# rows, groups of at most and of more than a row tile; long blocks
+FORMS = {
+    "rows": dict(new=[1] * 40, past=[30 + b for b in range(40)], L=1, H=1, G=1, mem=[20, 30, 10]),
+    "memory": dict(new=[1] * 40, past=[30 + b for b in range(40)], L=8, H=16, G=4, mem=[200, 300, 50]),
+    "memory, two row tiles": dict(new=[1] * 40, past=[30 + b for b in range(40)], L=8, H=16, G=8, mem=[200, 300, 50]),
+    "memory, drafts": dict(new=[3] * 40, past=[30 + b for b in range(40)], L=8, H=16, G=4, mem=[400, 300, 350]),
+    "blocks": dict(new=[20] * 40, past=[3 + b for b in range(40)], L=2, H=16, G=4, mem=[100, 130, 50]),
+}
+GROUPS = [0, 12, 25, 40]
+
+
+def _batch(form):
+    case = FORMS[form]
+    mem = [[m - l for l in range(case["L"])] for m in case["mem"]]
+    x = Batch(**{**case, "mem": mem}, groups=GROUPS, seed=61)
+    assert [f[0] for f in forms(x)] == {"rows": ["rows"], "blocks": ["blocks"]}.get(form, ["memory", "rows"])
+    x.out.fill_(7.0)
+    return x
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("at,value,lost", [(0, -1, [0]), (1, 99, [0, 1]), (1, -5, [0, 1]), (2, 2000, [1, 2]), (3, 41, [2])])
+def test_attend_one_bad_group_offset(form, at, value, lost):
+    # the groups on both sides of it have no memory, the third keeps its own
+    x = _batch(form)
+    x.goff[at] = value
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_OFFSETS
+    group_of = x.group_of
+    x.group_of = lambda b: None if group_of(b) in lost else group_of(b)
+    want, tol = x.attend()
+    assert ((x.out.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("form", ["memory", "memory, two row tiles", "memory, drafts", "blocks"])
+def test_attend_device_conditions(form):
+    x = _batch(form)
+    good = x.table.clone()
+    x.mem_len[1, 0] += 200                      # clamped
+    x.table[3, 0] = x.n_pages                   # rows 0..15 of sequence 3 are not seen
+    x.call_attend(msa)
+    x.mem_len[1, 0] = min(x.mem_len[1, 0].item(), x.M)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_PAGE | msa.MSA_DEVERR_CAPACITY
+    x.mem.nan_to_num_(0.25)
+    x.call_attend(msa)
+    rest = [b for b in range(40) if b != 3]
+    want, tol = x.attend(only=rest)
+    assert ((x.out.double() - want).abs() <= tol)[tol >= 0].all()
+    assert not x.out[:, x.off[3]:x.off[4]].isnan().any()
+    x.table.copy_(good)
+    x.err.zero_()
+    x.seq_len[5] = x.max_pages * x.page + 3     # clamped to the table's rows
+    x.pages.nan_to_num_(0.25)
+    spare = [i for i in range(x.n_pages) if all(i not in r for r in x.ids)]
+    x.ids[5] = (x.ids[5] + spare * x.max_pages)[:x.max_pages]
+    x.table[5] = torch.tensor(x.ids[5], dtype=torch.int32)
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_LOCAL_FULL
+    want, tol = x.attend()
+    assert ((x.out.double() - want).abs() <= tol).all()

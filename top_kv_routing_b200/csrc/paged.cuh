@@ -145,4 +145,27 @@ __device__ __forceinline__ int find_last(const int32_t* __restrict__ off, int B,
   }
 }
 
+// Whether group g's offsets are usable.
+__device__ __forceinline__ bool group_usable(const Attend& a, int g) {
+  const int s = a.group_offsets[g], e = a.group_offsets[g + 1];
+  return s >= 0 && e >= s && e <= a.B;
+}
+
+// The group of sequence b, -1 for none (the lanes of a warp together): the last usable one that
+// holds it.  in_order: all groups are usable, so none share a sequence.
+__device__ __forceinline__ int group_of(const Attend& a, int b, bool in_order, int lane) {
+  if (in_order) {
+    const int g = a.NG > 0 ? find_last(a.group_offsets, a.NG, b, lane) : -1;
+    return g >= 0 && b < a.group_offsets[g + 1] ? g : -1;
+  }
+  int found = -1;
+  for (int g0 = 0; g0 < a.NG; g0 += 32) {
+    const int g = g0 + lane;
+    const bool holds = g < a.NG && group_usable(a, g) && a.group_offsets[g] <= b && b < a.group_offsets[g + 1];
+    const unsigned m = __ballot_sync(0xffffffffu, holds);
+    if (m) found = g0 + 31 - __clz(m);
+  }
+  return found;
+}
+
 }  // namespace paged

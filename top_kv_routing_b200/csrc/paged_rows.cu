@@ -61,6 +61,7 @@ struct Tables {
   int gmt[kMaxSeqs];           // memory tiles of a group's longest layer (PART: partial slots per split)
   int goff[kMaxSeqs + 1];      // group offsets
   int64_t warp_sum[kRowWarps];
+  int by_sequence;             // PART: the memory kernel took each sequence's tokens by themselves
 };
 
 // Whether this lane's eighth of a warp's 16 bf16 rows at `st` holds an infinity or a NaN.
@@ -154,9 +155,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const bool groups_ok = __syncthreads_and(ok);
   if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-  for (int gr = warp; gr < a.NG && groups_ok; gr += kRowWarps) {
+  if (tid == 0) tb.by_sequence = !groups_ok;
+  for (int gr = warp; gr < a.NG; gr += kRowWarps) {
     const int s = tb.goff[gr], e = tb.goff[gr + 1];
-    if (PART) {
+    if (!groups_ok) {
+      // each usable group by itself; of several that hold a sequence the last (in every CTA: the
+      // pieces of the line have to agree)
+      for (int b = s + lane; s >= 0 && e <= a.B && b < e; b += 32) atomicMax(&tb.grp[b], gr);
+    } else if (PART) {
       // partial slots per split: two where the group's rows fit one row tile, none where the
       // memory kernel left the group out
       const int lo = tb.tok0[s], hi = tb.tok0[e];
@@ -646,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait_for_earlier_kernels();
           memory_done = true;
         }
-        const int slots = __ldcg(reinterpret_cast<const int*>(a.ws + kWsSplits)) * tb.gmt[tb.grp[c.b]];
+        const int per_split = tb.by_sequence ? (tb.n[c.b] <= 128 / G ? 2 : 1) : tb.gmt[tb.grp[c.b]];
+        const int slots = __ldcg(reinterpret_cast<const int*>(a.ws + kWsSplits)) * per_split;
         const int64_t all_rows = (int64_t)a.L * a.T * Hq;
         join(slots, reinterpret_cast<const float2*>(a.ws + kWsMemory + memory_part_bytes(all_rows, max_splits)),
              reinterpret_cast<const float*>(a.ws + kWsMemory),

@@ -2,7 +2,8 @@
 // forms (msa_paged.h defines the result):
 //   memory form  the packed tokens of a group (all of its sequences' new tokens) x the G query
 //                heads of key head h are the MMA's rows, so every tile of the group's memory is
-//                read once per 256 rows whatever the number of sequences.  A unit is (group,
+//                read once per 256 rows whatever the number of sequences.  (Where offsets are
+//                unusable, the tokens of each sequence by themselves.)  A unit is (group,
 //                layer, key head, pair of row tiles, key split); its result per row and split,
 //                the unnormalised fp32 output, its maximum and its sum, is joined with the
 //                sequence's own pages by the row kernel (paged_rows.cu).
@@ -100,7 +101,7 @@ struct Unit {
   int poison;                // block form: values that are not finite were taken out of its tiles
 };
 
-// Shared variables.  An entry is a group (memory form) or a sequence (block form).
+// Shared variables.  An entry is a group (memory form as a rule) or a sequence.
 constexpr int kBlocks = kMaxSeqs / 32;
 static_assert(kBlocks <= 32, "a lane per block of entries");
 struct TablesTc {
@@ -290,16 +291,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   let_next_kernel_start();
 
   // ---- the batch: row-tile pairs, most key tiles
-  const int n_entries = BLOCK ? a.B : a.NG, n_blocks = (n_entries + 31) / 32;
+  // (memory form: by group as a rule, by sequence where groups have unusable offsets and may overlap)
+  bool by_sequence = BLOCK;
   const int64_t cap = (int64_t)a.max_pages << a.log2_page;
   // what the batch needs is asked for at once: memory lengths, offsets of groups, tokens
   int most = 0;
   for (int i = tid; i < a.NG * a.L; i += kThreadsTc) most = max(most, a.mem_len[i]);
   bool ok_here = true;  // the group offsets are non-decreasing within [0, B]
-  for (int g = tid; g < a.NG; g += kThreadsTc) {
-    const int s = a.group_offsets[g], e = a.group_offsets[g + 1];
-    ok_here &= s >= 0 && e >= s && e <= a.B;
-  }
+  for (int g = tid; g < a.NG; g += kThreadsTc) ok_here &= group_usable(a, g);
   auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
   int32_t* order = reinterpret_cast<int32_t*>(a.ws + kWsOrder);  // (every CTA writes the same)
   if (BLOCK) {
@@ -331,20 +330,27 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     fence_async_smem();  // (the tiles come through the async proxy)
     __syncthreads();
   }
-  for (int k = warp; k < n_blocks; k += kWarpsTc) {
-    const int e = 32 * k + lane;
-    int lo = 0, n = 0;
-    if (e < n_entries) {
-      if (BLOCK) {
-        sequence_tokens(a.q_offsets, order[e], a.T, lo, n);
-      } else {
-        const int s = a.group_offsets[e], f = a.group_offsets[e + 1];
-        if (s >= 0 && f >= s && f <= a.B) group_tokens(a, e, lo, n);
-      }
+  // tokens of entry e (block form: the e-th sequence in order); none where they are unusable
+  auto entry_tokens = [&](int e, int& lo, int& n) {
+    lo = n = 0;
+    if (by_sequence)
+      sequence_tokens(a.q_offsets, BLOCK ? order[e] : e, a.T, lo, n);
+    else if (group_usable(a, e))
+      group_tokens(a, e, lo, n);
+  };
+  int n_entries, n_blocks;
+  auto count_pairs = [&]() {
+    n_entries = by_sequence ? a.B : a.NG;
+    n_blocks = (n_entries + 31) / 32;
+    for (int k = warp; k < n_blocks; k += kWarpsTc) {
+      const int e = 32 * k + lane;
+      int lo = 0, n = 0;
+      if (e < n_entries) entry_tokens(e, lo, n);
+      const int sum = __reduce_add_sync(0xffffffffu, pairs_of(n));
+      if (lane == 0) tb.scan[k] = sum;
     }
-    const int sum = __reduce_add_sync(0xffffffffu, pairs_of(n));
-    if (lane == 0) tb.scan[k] = sum;
-  }
+  };
+  count_pairs();
   if (most > a.M_max) {
     if (blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_CAPACITY);
     most = a.M_max;
@@ -352,17 +358,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0) atomicMax(&tb.most, (most + kTile - 1) / kTile);
   tc_fence_before();
-  const bool groups_ok = __syncthreads_and(ok_here);  // (where they are not, no group has a unit)
+  const bool groups_ok = __syncthreads_and(ok_here);
   tc_fence_after();
   if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-  // tokens of entry e (block form: the e-th sequence in order); false where they are unusable
-  auto entry_tokens = [&](int e, int& lo, int& n) -> bool {
-    if (BLOCK) return sequence_tokens(a.q_offsets, order[e], a.T, lo, n);
-    lo = n = 0;
-    return groups_ok && group_tokens(a, e, lo, n);
-  };
+  if (!BLOCK && !groups_ok) {
+    by_sequence = true;
+    count_pairs();
+    __syncthreads();
+  }
   if (warp == 0) {  // sums before each block, and the split
-    const int v = lane < n_blocks && (BLOCK || groups_ok) ? tb.scan[lane] : 0;
+    const int v = lane < n_blocks ? tb.scan[lane] : 0;
     int inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -439,11 +444,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     lo = __shfl_sync(0xffffffffu, lo, from);
     n = __shfl_sync(0xffffffffu, n, from);
     const int at = (pair - __shfl_sync(0xffffffffu, before, from)) * 2 * kTok;
-    int g = x.e;
-    if (BLOCK) {
-      g = a.NG > 0 && groups_ok ? find_last(a.group_offsets, a.NG, x.e, lane) : -1;
-      if (g >= 0 && x.e >= a.group_offsets[g + 1]) g = -1;
-    }
+    const int g = by_sequence ? group_of(a, x.e, groups_ok, lane) : x.e;
     const int64_t gl = (int64_t)g * a.L + x.l;
     x.M = g < 0 ? 0 : max(0, min(a.M_max, __ldg(a.mem_len + gl)));
     x.kv_row = (gl * 2 * a.H + x.h) * a.M_max;
