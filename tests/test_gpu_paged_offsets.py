@@ -43,6 +43,23 @@ def _batch(form):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("at,value", [(12, 100000), (12, -3), (25, 0), (18, 100000), (18, 0), (0, -1), (40, 100000),
+                                      (39, -7)])
+def test_attend_one_bad_token_offset(form, at, value):
+    # an offset at a border between groups, inside a group, the first and the last one
+    x = _batch(form)
+    x.off[at] = value
+    x.call_attend(msa)
+    assert x.err.item() == msa.MSA_DEVERR_BAD_OFFSETS
+    if value == 0:
+        # sequence `at` is [0, ...): it shares its tokens with the ones before it, which are then undefined
+        want, tol = x.attend(only=range(at + 1, 40))
+        assert ((x.out.double() - want).abs() <= tol)[tol >= 0].all() and (tol >= 0).any()
+        return
+    _check_only(x, [b for b in range(40) if b not in (at - 1, at)])
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("at,value,lost", [(0, -1, [0]), (1, 99, [0, 1]), (1, -5, [0, 1]), (2, 2000, [1, 2]), (3, 41, [2])])
 def test_attend_one_bad_group_offset(form, at, value, lost):
     # the groups on both sides of it have no memory, the third keeps its own

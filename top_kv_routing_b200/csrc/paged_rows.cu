@@ -124,12 +124,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tb.goff[g] = g == tid ? g_first : a.group_offsets[g];
     if (g < a.NG) tb.gmt[g] = 0;
   }
+  bool ok = true;  // all offsets are usable
   for (int b = tid; b < a.B; b += kThreads) {
     const int lo = b == tid ? lo_first : a.q_offsets[b], hi = b == tid ? hi_first : a.q_offsets[b + 1];
     const int len = b == tid ? len_first : a.seq_len[b];
     const bool usable = lo >= 0 && hi >= lo && hi <= a.T;
     const int n = usable ? hi - lo : 0;
-    if (!usable && blockIdx.x == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+    ok &= usable;
     if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
     tb.tok0[b] = lo;
     if (b == a.B - 1) tb.tok0[a.B] = hi;
@@ -138,7 +139,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tb.grp[b] = -1;
   }
   __syncthreads();
-  bool ok = true;
   for (int g = tid; g < a.NG; g += kThreads) {
     const int s = tb.goff[g], e = tb.goff[g + 1];
     ok &= s >= 0 && e >= s && e <= a.B;
@@ -153,23 +153,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (m > 0) atomicMax(&tb.gmt[i / a.L], (m + kTileKeys - 1) / kTileKeys);
     }
   }
-  const bool groups_ok = __syncthreads_and(ok);
-  if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-  if (tid == 0) tb.by_sequence = !groups_ok;
+  const bool offsets_ok = __syncthreads_and(ok);
+  if (!offsets_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+  if (tid == 0) tb.by_sequence = !offsets_ok;
   for (int gr = warp; gr < a.NG; gr += kRowWarps) {
     const int s = tb.goff[gr], e = tb.goff[gr + 1];
-    if (!groups_ok) {
+    if (!offsets_ok) {
       // each usable group by itself; of several that hold a sequence the last (in every CTA: the
       // pieces of the line have to agree)
       for (int b = s + lane; s >= 0 && e <= a.B && b < e; b += 32) atomicMax(&tb.grp[b], gr);
     } else if (PART) {
-      // partial slots per split: two where the group's rows fit one row tile, none where the
-      // memory kernel left the group out
-      const int lo = tb.tok0[s], hi = tb.tok0[e];
-      const bool in = lo >= 0 && hi >= lo && hi <= a.T;
-      for (int b = s + lane; b < e && in; b += 32)
-        if (tb.tok0[b] >= lo && tb.tok0[b] + tb.n[b] <= hi) tb.grp[b] = gr;
-      if (lane == 0) tb.gmt[gr] = !in ? 0 : hi - lo <= 128 / G ? 2 : 1;
+      for (int b = s + lane; b < e; b += 32) tb.grp[b] = gr;
+      // partial slots per split: two where the group's rows fit one row tile
+      if (lane == 0) tb.gmt[gr] = tb.tok0[e] - tb.tok0[s] <= 128 / G ? 2 : 1;
     } else {
       for (int b = s + lane; b < e; b += 32) tb.grp[b] = gr;
     }

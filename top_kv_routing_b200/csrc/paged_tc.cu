@@ -291,14 +291,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   let_next_kernel_start();
 
   // ---- the batch: row-tile pairs, most key tiles
-  // (memory form: by group as a rule, by sequence where groups have unusable offsets and may overlap)
+  // (memory form: by group as a rule, by sequence where offsets are unusable: groups may overlap then,
+  // and a group's first and last offset may be the unusable ones)
   bool by_sequence = BLOCK;
   const int64_t cap = (int64_t)a.max_pages << a.log2_page;
   // what the batch needs is asked for at once: memory lengths, offsets of groups, tokens
   int most = 0;
   for (int i = tid; i < a.NG * a.L; i += kThreadsTc) most = max(most, a.mem_len[i]);
-  bool ok_here = true;  // the group offsets are non-decreasing within [0, B]
+  bool ok_here = true;  // the group offsets are usable (memory form: and the sequences')
   for (int g = tid; g < a.NG; g += kThreadsTc) ok_here &= group_usable(a, g);
+  int lo, n;
+  for (int b = tid; b < a.B && !BLOCK; b += kThreadsTc) ok_here &= sequence_tokens(a.q_offsets, b, a.T, lo, n);
   auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
   int32_t* order = reinterpret_cast<int32_t*>(a.ws + kWsOrder);  // (every CTA writes the same)
   if (BLOCK) {
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     int* size = reinterpret_cast<int*>(smem + kOffRing);
     for (int e = tid; e < a.B; e += kThreadsTc) {
       const int len = a.seq_len[e];
-      int lo, n, from = 0, to = a.NG;  // the group: from <= it < to (whatever the offsets hold)
+      int from = 0, to = a.NG;  // the group: from <= it < to (whatever the offsets hold)
       if (!sequence_tokens(a.q_offsets, e, a.T, lo, n) && blockIdx.x == 0)
         msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
       if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
@@ -358,10 +361,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   most = __reduce_max_sync(0xffffffffu, most);
   if (lane == 0) atomicMax(&tb.most, (most + kTile - 1) / kTile);
   tc_fence_before();
-  const bool groups_ok = __syncthreads_and(ok_here);
+  const bool offsets_ok = __syncthreads_and(ok_here);
   tc_fence_after();
-  if (!groups_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
-  if (!BLOCK && !groups_ok) {
+  if (!offsets_ok && blockIdx.x == 0 && tid == 0) msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
+  if (!BLOCK && !offsets_ok) {
     by_sequence = true;
     count_pairs();
     __syncthreads();
@@ -444,7 +447,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     lo = __shfl_sync(0xffffffffu, lo, from);
     n = __shfl_sync(0xffffffffu, n, from);
     const int at = (pair - __shfl_sync(0xffffffffu, before, from)) * 2 * kTok;
-    const int g = by_sequence ? group_of(a, x.e, groups_ok, lane) : x.e;
+    const int g = by_sequence ? group_of(a, x.e, offsets_ok, lane) : x.e;
     const int64_t gl = (int64_t)g * a.L + x.l;
     x.M = g < 0 ? 0 : max(0, min(a.M_max, __ldg(a.mem_len + gl)));
     x.kv_row = (gl * 2 * a.H + x.h) * a.M_max;
