@@ -99,3 +99,33 @@ def test_attend_device_conditions(form):
     assert x.err.item() == msa.MSA_DEVERR_LOCAL_FULL
     want, tol = x.attend()
     assert ((x.out.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("B", [4, 33, 100, 1024])
+@pytest.mark.parametrize("value", [-5, 0, 100000])
+def test_append_stores_the_tokens_of_usable_sequences(B, value):
+    # one bad offset in turn at every place that a search of the offsets may look at
+    for at in sorted({1, 2, B // 2, B - 2, B - 1} | set(range(0, B, max(1, -(-B // 32) * 5)))):
+        if at == 0 and value == 0:
+            continue
+        x = Batch([1] * B, [b % 15 for b in range(B)], H=1, G=1, page=16, pad=2, seed=62)
+        before, q_rot = x.pages.clone(), torch.full_like(x.out, 7.0)
+        x.off[at] = value
+        if at == 1 and value == 0:  # (sequence 0 without tokens, sequence 1 with two: nothing is wrong)
+            continue
+        x.call_append(msa, q_rot=q_rot)
+        assert x.err.item() & msa.MSA_DEVERR_BAD_OFFSETS
+        skip = {at - 1, at}
+        good = torch.tensor([b for b in range(B) if b not in skip and (value != 0 or b > at)], dtype=torch.long)
+        row = torch.tensor([b % 15 for b in range(B)])[good]
+        ids = torch.tensor([x.ids[b][0] for b in good.tolist()], dtype=torch.long)
+        want = rope(x.q[0, good].cpu(), 16 + row)
+        assert ((q_rot[0, good].cpu().double() - want).abs() <= want.abs() * 2 ** -8 + 2 ** -15).all(), (at, value)
+        assert torch.equal(x.pages[0, ids, 1, 0, row].cpu(), x.v[0, good, 0].cpu()), (at, value)
+        if value != 0:
+            left = [b for b in range(B) if b in skip]
+            assert (q_rot[0, left] == 7.0).all() and (q_rot[0, -2:] == 7.0).all()
+            own = torch.zeros(x.n_pages, dtype=torch.bool)
+            own[ids] = True
+            a, b = x.pages[0, ~own].nan_to_num(9.0), before[0, ~own].nan_to_num(9.0)
+            assert torch.equal(a, b), (at, value)

@@ -206,9 +206,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   Row r;
   if (x.li < nl) r = load(x);
   if (warp == 0) {
-    int b = find_last(a.off, a.B, t, lane);
     int b0 = 0, n = 0;
-    if (b >= 0 && (!sequence_tokens(a.off, b, a.T, b0, n) || t < b0 || t >= b0 + n)) b = -1;
+    const int b = sequence_of(a.off, a.B, a.T, t, lane, b0, n);
     int64_t row = -1;
     if (b >= 0) {
       const long long i = (long long)a.seq_len[b] - n + (t - b0);

@@ -145,6 +145,24 @@ __device__ __forceinline__ int find_last(const int32_t* __restrict__ off, int B,
   }
 }
 
+// The sequence of token t, whose tokens are then [lo, lo + n), -1 for none (the lanes of a warp
+// together): by the search above, and one after the other where that finds none, since an unusable
+// offset may have misled it (the last usable sequence that holds t).
+__device__ __forceinline__ int sequence_of(const int32_t* __restrict__ off, int B, int T, int t, int lane, int& lo,
+                                           int& n) {
+  const int b = find_last(off, B, t, lane);
+  if (b >= 0 && sequence_tokens(off, b, T, lo, n) && t < lo + n) return b;  // (lo <= t by the search)
+  int found = -1;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    int first, count;
+    const bool holds = b0 + lane < B && sequence_tokens(off, b0 + lane, T, first, count) && t >= first && t < first + count;
+    const unsigned m = __ballot_sync(0xffffffffu, holds);
+    if (m) found = b0 + 31 - __clz(m);
+  }
+  if (found >= 0) sequence_tokens(off, found, T, lo, n);
+  return found;
+}
+
 // Whether group g's offsets are usable.
 __device__ __forceinline__ bool group_usable(const Attend& a, int g) {
   const int s = a.group_offsets[g], e = a.group_offsets[g + 1];
