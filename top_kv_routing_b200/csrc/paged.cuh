@@ -169,13 +169,9 @@ __device__ __forceinline__ bool group_usable(const Attend& a, int g) {
   return s >= 0 && e >= s && e <= a.B;
 }
 
-// The group of sequence b, -1 for none (the lanes of a warp together): the last usable one that
-// holds it.  in_order: all groups are usable, so none share a sequence.
-__device__ __forceinline__ int group_of(const Attend& a, int b, bool in_order, int lane) {
-  if (in_order) {
-    const int g = a.NG > 0 ? find_last(a.group_offsets, a.NG, b, lane) : -1;
-    return g >= 0 && b < a.group_offsets[g + 1] ? g : -1;
-  }
+// The last usable group that holds sequence b, -1 for none (the lanes of a warp together).  Apart
+// from the kernels' code: only unusable offsets lead here.
+static __device__ __noinline__ int last_group_of(const Attend& a, int b, int lane) {
   int found = -1;
   for (int g0 = 0; g0 < a.NG; g0 += 32) {
     const int g = g0 + lane;

@@ -296,12 +296,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   bool by_sequence = BLOCK;
   const int64_t cap = (int64_t)a.max_pages << a.log2_page;
   // what the batch needs is asked for at once: memory lengths, offsets of groups, tokens
+  const bool check = !BLOCK && tid < a.B;
+  const int lo_first = check ? a.q_offsets[tid] : 0, hi_first = check ? a.q_offsets[tid + 1] : 0;
   int most = 0;
   for (int i = tid; i < a.NG * a.L; i += kThreadsTc) most = max(most, a.mem_len[i]);
   bool ok_here = true;  // the group offsets are usable (memory form: and the sequences')
-  for (int g = tid; g < a.NG; g += kThreadsTc) ok_here &= group_usable(a, g);
-  int lo, n;
-  for (int b = tid; b < a.B && !BLOCK; b += kThreadsTc) ok_here &= sequence_tokens(a.q_offsets, b, a.T, lo, n);
+  for (int g = tid; g < a.NG; g += kThreadsTc) {
+    const int s = a.group_offsets[g], e = a.group_offsets[g + 1];
+    ok_here &= s >= 0 && e >= s && e <= a.B;
+  }
+  ok_here &= lo_first >= 0 && hi_first >= lo_first && hi_first <= a.T;
+  for (int b = tid + kThreadsTc; b < a.B && !BLOCK; b += kThreadsTc) {
+    int lo, n;
+    ok_here &= sequence_tokens(a.q_offsets, b, a.T, lo, n);
+  }
   auto pairs_of = [](int n) -> int { return (n + 2 * kTok - 1) / (2 * kTok); };
   int32_t* order = reinterpret_cast<int32_t*>(a.ws + kWsOrder);  // (every CTA writes the same)
   if (BLOCK) {
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     int* size = reinterpret_cast<int*>(smem + kOffRing);
     for (int e = tid; e < a.B; e += kThreadsTc) {
       const int len = a.seq_len[e];
-      int from = 0, to = a.NG;  // the group: from <= it < to (whatever the offsets hold)
+      int lo, n, from = 0, to = a.NG;  // the group: from <= it < to (whatever the offsets hold)
       if (!sequence_tokens(a.q_offsets, e, a.T, lo, n) && blockIdx.x == 0)
         msa::set_err(a.dev_err, MSA_DEVERR_BAD_OFFSETS);
       if (blockIdx.x == 0 && n > 0 && len > cap) msa::set_err(a.dev_err, MSA_DEVERR_LOCAL_FULL);
@@ -447,7 +455,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     lo = __shfl_sync(0xffffffffu, lo, from);
     n = __shfl_sync(0xffffffffu, n, from);
     const int at = (pair - __shfl_sync(0xffffffffu, before, from)) * 2 * kTok;
-    const int g = by_sequence ? group_of(a, x.e, offsets_ok, lane) : x.e;
+    int g = x.e;
+    if (by_sequence && offsets_ok) {
+      g = a.NG > 0 ? find_last(a.group_offsets, a.NG, x.e, lane) : -1;
+      if (g >= 0 && x.e >= a.group_offsets[g + 1]) g = -1;
+    } else if (by_sequence) {
+      g = last_group_of(a, x.e, lane);
+    }
     const int64_t gl = (int64_t)g * a.L + x.l;
     x.M = g < 0 ? 0 : max(0, min(a.M_max, __ldg(a.mem_len + gl)));
     x.kv_row = (gl * 2 * a.H + x.h) * a.M_max;
