@@ -540,10 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         sum[v] += __shfl_xor_sync(0xffffffffu, sum[v], 2);
       }
       if (NR == 1) {
+        // (an infinite value times a residual of zero or below zero would make the row's infinity a NaN)
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          o[n][0] += o[n][2];
-          o[n][1] += o[n][3];
+          o[n][0] += fabsf(o[n][0]) < INFINITY ? o[n][2] : 0.f;
+          o[n][1] += fabsf(o[n][1]) < INFINITY ? o[n][3] : 0.f;
         }
       }
       // Joins `n` partial results (place(i, r): of row r the i-th one's index) to what the rows
