@@ -153,6 +153,27 @@ def _ptr(t) -> int | None:
         return t.ctypes.data
 
 
+_DTYPES: dict = {}  # dtype -> MSA_F32 or MSA_BF16
+
+
+def _dtype(where: str, *tensors) -> int:
+    """The msa_dtype of the tensors (None is skipped), which must all have it."""
+    code = None
+    for t in tensors:
+        if t is None:
+            continue
+        c = _DTYPES.get(t.dtype)
+        if c is None:
+            name = str(t.dtype)
+            if name.startswith("torch.") and name not in ("torch.bfloat16", "torch.float32"):
+                raise MsaError(MSA_ERR_UNSUPPORTED, where, f"{name}: bfloat16 or float32 tensors")
+            c = _DTYPES[t.dtype] = MSA_BF16 if name == "torch.bfloat16" else MSA_F32
+        if code is not None and c != code:
+            raise MsaError(MSA_ERR_INVALID_ARG, where, "tensors of different types")
+        code = c
+    return code
+
+
 def _nbytes(t) -> int:
     if t is None:
         return 0
@@ -190,8 +211,7 @@ def msa_pool_blocks(k, v, kr, doc_tok_offsets, doc_chunk_offsets, n_docs: int, n
                     head_dim: int, chunk: int, rope_theta: float, k_bar=None, v_bar=None, kr_hat=None,
                     kr_norm=None, dev_err=None, in_dtype: int | None = None, stream=None):
     if in_dtype is None:
-        x = next(t for t in (k, v, kr) if t is not None)
-        in_dtype = MSA_BF16 if str(x.dtype) == "torch.bfloat16" else MSA_F32
+        in_dtype = _dtype("msa_pool_blocks", k, v, kr)
     st = pool_lib.msa_pool_blocks(_ptr(k), _ptr(v), _ptr(kr), in_dtype, _ptr(doc_tok_offsets),
                                   _ptr(doc_chunk_offsets), n_docs, n_chunks, n_heads, head_dim, chunk,
                                   rope_theta, _ptr(k_bar), _ptr(v_bar), _ptr(kr_hat), _ptr(kr_norm),
@@ -218,7 +238,7 @@ def msa_route_topk(qr, q_offsets, kr_hat, doc_chunk_offsets, n_docs: int, n_chun
     msa_route_filter_keys (needed by MSA_ROUTE_TENSOR_F8, picked by MSA_ROUTE_AUTO)."""
     qo = np.ascontiguousarray(q_offsets, dtype=np.int32)
     if q_dtype is None:
-        q_dtype = MSA_BF16 if str(qr.dtype) == "torch.bfloat16" else MSA_F32
+        q_dtype = _dtype("msa_route_topk", qr)
     ws_bytes = _nbytes(workspace)
     st = route_lib.msa_route_topk(_ptr(qr), q_dtype, qo.ctypes.data, len(qo) - 1, _ptr(kr_hat), _ptr(kr_f8),
                                   _ptr(doc_chunk_offsets), n_docs, n_chunks, n_layers, n_q_heads, n_kv_heads,
@@ -351,7 +371,7 @@ def msa_paged_append(q, k_new, v_new, q_offsets, n_tokens: int, n_seqs: int, n_l
     the queries into q_rot (include/msa_paged.h).  q and q_rot may both be None; strides are
     elements from one token to the next, 0 for dense rows.  Returns the kernels enqueued."""
     if in_dtype is None:
-        in_dtype = MSA_BF16 if str(k_new.dtype) == "torch.bfloat16" else MSA_F32
+        in_dtype = _dtype("msa_paged_append", q, k_new, v_new)
     st = paged_lib.msa_paged_append(_ptr(q), _ptr(k_new), _ptr(v_new), in_dtype, q_stride, k_stride, v_stride,
                                     _ptr(q_offsets), n_tokens, n_seqs, n_layers, n_q_heads, n_kv_heads, head_dim,
                                     _ptr(kv_pages), n_pages, page_size, _ptr(page_table), max_pages, _ptr(seq_len),
