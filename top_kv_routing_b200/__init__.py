@@ -8,13 +8,14 @@ ImportError if the libraries have not been built (``python top_kv_routing_b200/b
 from __future__ import annotations
 
 import importlib
+import sys
 
 _SUBMODULES = {"abi", "build", "engine"}
+_ABI = __name__ + ".abi"
 
 
 def __getattr__(name: str):
     if name.startswith("__") or name in _SUBMODULES:
         raise AttributeError(name)
-    value = getattr(importlib.import_module(__name__ + ".abi"), name)
-    globals()[name] = value  # (found without this function from now on: it costs 1 us)
-    return value
+    # (looked up in `abi` each time, so that what is replaced there is replaced here)
+    return getattr(sys.modules.get(_ABI) or importlib.import_module(_ABI), name)
