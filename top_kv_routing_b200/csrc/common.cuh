@@ -7,6 +7,8 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <atomic>
+
 #include "msa_common.h"
 
 // Each library defines its own thread-local last-error buffer and accessor.
@@ -36,28 +38,30 @@ namespace msa {
 // Returns 1 when the current device is sm_100 (B200), 0 when it is another device and
 // -1 when no device can be queried.  Cached per device ordinal.
 inline int current_device_is_sm100(int* dev_out) {
-  static int cache[64];  // 0 unknown, 1 yes, 2 no
+  static std::atomic<int> cache[64];  // 0 unknown, 1 yes, 2 no
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
   if (dev_out) *dev_out = dev;
-  if (dev >= 0 && dev < 64 && cache[dev]) return cache[dev] == 1;
+  const int known = dev >= 0 && dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
+  if (known) return known == 1;
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return -1;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return -1;
   const int ok = (major == 10 && minor == 0) ? 1 : 2;
-  if (dev >= 0 && dev < 64) cache[dev] = ok;
+  if (dev >= 0 && dev < 64) cache[dev].store(ok, std::memory_order_relaxed);
   return ok == 1;
 }
 
 // Cached per device ordinal, as above.
 inline int sm_count() {
-  static int cache[64];
-  int dev = 0, n = 148;
+  static std::atomic<int> cache[64];
+  int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  if (dev >= 0 && dev < 64 && cache[dev]) return cache[dev];
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (n <= 0) n = 148;
-  if (dev >= 0 && dev < 64) cache[dev] = n;
+  const bool cached = dev >= 0 && dev < 64;
+  if (cached) n = cache[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (cached) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
