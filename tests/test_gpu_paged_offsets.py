@@ -129,3 +129,20 @@ def test_append_stores_the_tokens_of_usable_sequences(B, value):
             own[ids] = True
             a, b = x.pages[0, ~own].nan_to_num(9.0), before[0, ~own].nan_to_num(9.0)
             assert torch.equal(a, b), (at, value)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_batches_without_tokens(form):
+    # every sequence empty (all tokens padding): nothing is written, and the workspace stays ready
+    x = _batch(form)
+    off = x.off.clone()
+    pages, q_rot = x.pages.clone(), torch.full_like(x.out, 7.0)
+    for value in (0, 7, x.T):
+        x.off.fill_(value)
+        x.call_append(msa, q_rot=q_rot)
+        x.call_attend(msa)
+    assert (x.out == 7.0).all() and (q_rot == 7.0).all() and x.err.item() == 0
+    assert torch.equal(x.pages.view(torch.int16), pages.view(torch.int16))
+    x.off.copy_(off)
+    x.call_attend(msa)
+    x.check()
