@@ -83,7 +83,9 @@ msa_status msa_shared_attend_workspace_size(int32_t n_tokens, int32_t n_seqs, in
  *   out[l][t][hq] = softmax(softmax_scale * <q_hq, K_j>) . V_j, key head h = hq / G, and 0
  *                   for a token that sees no key at all
  * (fp32 scores, maxima and sums; the weights may be rounded to bf16 for the tensor cores, the
- * output is rounded to bf16).
+ * output is rounded to bf16).  The kernels, and with them the weights' rounding and the time, are
+ * chosen from the sizes given (n_tokens, n_seqs, n_groups, heads, layers, max_mem_chunks,
+ * max_pages * page_size), not from the lengths in use.
  *   q       DEVICE bf16 [n_layers][n_tokens][n_q_heads][head_dim], already rotated (q_rot)
  *   mem_kv  DEVICE bf16 [n_groups][n_layers][2][n_kv_heads][max_mem_chunks][head_dim]
  *           (msa_gather_kv output of n_groups queries); mem_len DEVICE int32 [n_groups][n_layers];

@@ -43,12 +43,20 @@ bool memory_form_open(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t G, in
 // (16 keys, row tile) of the row kernel with all warps at work, six of them for a row tile's own
 // costs and ten where the memory's results are joined to it; 3,100 per 128 keys and 5,000 per unit
 // of the tensor-core kernel; 20,000 for each kernel of the first two forms to start and end, 15,000
-// for the third.  The lengths are the largest ones that the buffers allow.  Of 228 batches of all
-// sizes, timed in every form that they may take, 223 got a form within 12 % of the best, 1 % from
-// it on average.  Both sides of the borders (us): 16 answers over 256 + 320 keys, 18 layers: memory
-// 99, rows 94; 33 drafts of 20 rows over 1,000 + 500 keys, 4 layers: memory 124, rows 180, blocks
-// 176; 128 answers in 16 groups: memory 450, rows 840; 47 tokens of 40 sequences over 500 + 250
-// keys, 6 layers: blocks 158, memory 216, rows 268.
+// for the third.  Of 228 batches of all sizes in buffers of just the lengths in use, timed in every
+// form that they may take, 223 got a form within 12 % of the best, 1 % from it on average.  Both
+// sides of the borders (us, 32 / 8 heads, cold): 16 answers over 256 + 300 keys, one layer: rows 20,
+// blocks 22, memory 27; 18 layers: rows 94, memory 100 (taken), blocks 164; 128 answers in 16 groups
+// over 400 + 215 keys, 18 layers: memory 451, rows 843, blocks 1,350; 40 sequences of 8 tokens over
+// 500 + 250 keys, 6 layers: memory 150, rows 174, blocks 180; of 12 tokens: blocks 186, memory 209
+// (taken), rows 258; of 15: blocks 186, memory 266, rows 328.
+//
+// The lengths are the largest ones that the buffers allow (those in use are known to the device
+// alone), so room in the buffers moves the choice although it costs no form anything: over 256 + 300
+// keys in a memory of 2,048 rows and a table of 4,096, 4 sequences of 8 tokens and 4 layers take the
+// memory form, 44 against 21 of blocks; 16 of one token and one layer the memory form, 27 against
+// 20 of rows; 37 of 5 tokens over 1,000 + 500 keys with a table of 32,768 rows blocks, 192 against
+// 143 of memory.
 Plan plan_of(int64_t T, int64_t B, int64_t NG, int64_t L, int64_t Hq, int64_t H, int64_t mem_rows, int64_t page_rows) {
   const double G = (double)(Hq / H), rows = (double)T * G, units = (double)L * H, sms = 148;
   const double M = NG > 0 ? (double)mem_rows : 0., P = (double)page_rows;
@@ -104,7 +112,7 @@ const RopeFreq& rope_freq(float theta) {
 // stored.  Bound by HBM: every byte moves once (2.7 GB of long texts in 420 us, 0.99 of the copy
 // rate; one token 3.3 us in a graph).
 constexpr int kAppendThreads = 256;
-constexpr int kAppendCtas = 148 * 7;  // runs of layers are as long as leaves so many CTAs (five fit an SM)
+constexpr int kAppendCtas = 148 * 7;  // runs of layers are as long as leaves so many CTAs (five fit an SM at once)
 
 struct AppendArgs {
   const void *q, *k, *v;
