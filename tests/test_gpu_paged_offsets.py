@@ -146,3 +146,31 @@ def test_batches_without_tokens(form):
     x.off.copy_(off)
     x.call_attend(msa)
     x.check()
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_any_offsets_leave_the_workspace_ready(form):
+    # offsets of all kinds, many unusable, sequences that share tokens and groups that share
+    # sequences: no row past the tokens is written, and the next usable call is as ever
+    x = _batch(form)
+    x.call_attend(msa)
+    first, off, goff = x.out.clone(), x.off.clone(), x.goff.clone()
+    room = torch.full((x.out.numel() + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator().manual_seed(63)
+    for i in range(12):
+        bad = torch.randint(-3, x.T + 4, (41,), generator=gen, dtype=torch.int32)
+        if i % 3 == 0:  # mostly usable ones, some exchanged
+            bad = torch.where(torch.rand(41, generator=gen) < 0.2, bad, off.cpu())
+        if i % 3 == 1:  # every second sequence has all tokens
+            bad = torch.tensor([0, x.T] * 20 + [0], dtype=torch.int32)
+        x.off.copy_(bad)
+        x.goff.copy_(torch.randint(-2, 43, (4,), generator=gen, dtype=torch.int32) if i % 2 else goff)
+        x.out = room[:x.out.numel()].view(x.out.shape)
+        x.call_attend(msa)
+        torch.cuda.synchronize()
+        assert (room[x.out.numel():] == 7.0).all()
+        assert x.err.item() & ~(msa.MSA_DEVERR_BAD_OFFSETS) == 0
+        x.off.copy_(off)
+        x.goff.copy_(goff)
+        x.call_attend(msa)
+        assert torch.equal(first.view(torch.int16), x.out.view(torch.int16))
